@@ -60,7 +60,8 @@ typedef enum {
     PATH_ERR_UNSUPPORTED = 2, /* head dim or dtype this build does not handle */
     PATH_ERR_WORKSPACE = 3,   /* workspace null or smaller than required */
     PATH_ERR_CUDA = 4,        /* a kernel launch failed */
-    PATH_ERR_TIMEOUT = 5      /* a bounded device-side wait gave up (path_attn_wait_status) */
+    PATH_ERR_TIMEOUT = 5,     /* a bounded device-side wait gave up (path_attn_wait_status) */
+    PATH_ERR_PAGE = 6         /* paged cache: a page, slot or length out of range, or no page free */
 } path_status;
 
 /*
@@ -163,7 +164,8 @@ path_status path_attn_bwd(const void *q, const void *k, const void *v, const voi
  * `stream`, then returns PATH_ERR_TIMEOUT if the last path_attn_fwd /
  * path_attn_bwd that used `workspace` recorded such an event, PATH_ERR_WORKSPACE
  * if a reusing backward found the forward's saved quantities missing (see
- * path_attn_bwd), else PATH_OK (PATH_ERR_CUDA if the read-back itself fails).
+ * path_attn_bwd), PATH_ERR_PAGE if the last paged decode step that used it found a
+ * page, slot or length out of range, else PATH_OK (PATH_ERR_CUDA if the read-back itself fails).
  * It synchronises the host.
  */
 path_status path_attn_wait_status(const void *workspace, path_stream_t stream);
@@ -266,6 +268,152 @@ path_status path_attn_prefill(const void *q, const void *k, const void *v, const
                               int L, int d, path_dtype dt, void *out, float *lse, void *k_cache,
                               void *v_cache, float *g_cache, int capacity, void *workspace,
                               size_t workspace_bytes, path_stream_t stream);
+
+/*
+ * The paged decode cache: sequences of different lengths whose keys and values lie
+ * in pages of one pool, so that a batch can gain, lose and copy sequences without
+ * moving the others.
+ *
+ * A pool (one for each attention layer) holds n_pages pages of `page` rows for every
+ * head: k_pages, v_pages [n_pages, H, page, d] in the dtype, and with the forget gate
+ * g_pages [n_pages, H, page] fp32, all 16-byte aligned. The tables (one set for all
+ * layers) are int32 on the device:
+ *   table [n_slots, max_pages]  pages of each slot (sequence), in order of its rows;
+ *   held  [n_slots]             how many of these entries are in use;
+ *   lens  [n_slots]             rows filled so far;
+ *   owner [n_pages]             the table entry slot * max_pages + j that a page
+ *                               belongs to, or -1 for a free page.
+ * A page belongs to one entry: a decode step rewrites every key it attends to, so two
+ * sequences never share a page that they write. A prefix that many sequences continue
+ * lies in a slot of its own (path_decode_step_shared). New tables are table = -1,
+ * held = lens = 0, owner = -1.
+ *
+ * rows: [B] (or [n]) int32 slots; a negative one is an idle row, which is neither read
+ * nor written. No slot may stand twice in one call, except among the parents of a fork
+ * or state copy. What the tables say is checked on the device before it is used as an
+ * index: an out-of-range slot, length or page is never read or written, and is reported
+ * as each call says. Two calls on one pool or table, or with one workspace, have to be
+ * ordered (one stream, or events).
+ * page is a power of two from 16 to 1024; d in {64, 128}; dt PATH_F32 or PATH_BF16;
+ * n_pages * H * page, n_slots * max_pages and max_pages * page below 2^31;
+ * B * H <= 65535; at most 4096 rows in a reserve or fork. Beyond these:
+ * PATH_ERR_UNSUPPORTED.
+ */
+
+/*
+ * Workspace of path_decode_step_paged (prefix_len = 0) and path_decode_step_shared on the
+ * current device; 0 if the sizes are invalid or unsupported. A larger batch, table or
+ * prefix needs no less. 256-byte aligned.
+ */
+size_t path_decode_paged_workspace_bytes(int B, int H, int max_pages, int page, int d, path_dtype dt,
+                                         int prefix_len);
+
+/*
+ * One decode step of a ragged batch: path_decode_step (path_decode_step_gated with log_f
+ * and g_pages, which go together) for every batch row b with its own n = lens[slot],
+ * slot = rows[b] (b itself if rows is NULL, then B <= n_slots). q, k_new, v_new, w, out:
+ * [B,H,d], 16-byte aligned inputs; beta, log_f: [B,H] fp32. Row n of the slot is written
+ * with k_new, v_new (and g = 0); it needs a page, which path_pages_reserve gives. lens is
+ * not advanced: the caller does that once, after the last layer.
+ * A row whose slot, length (n < max_pages * page) or pages are out of range gets out = NaN
+ * and path_attn_wait_status reports PATH_ERR_PAGE; the rows of its sequence on valid pages
+ * may have been updated. A slot that stands twice gets NaN and the same report, and its
+ * cached rows are left undefined. Results do not depend on the order in which blocks run.
+ */
+path_status path_decode_step_paged(const void *q, const void *k_new, const void *v_new, const void *w,
+                                   const float *beta, const float *log_f, float scale, int B, int H,
+                                   int d, path_dtype dt, void *k_pages, void *v_pages, float *g_pages,
+                                   int n_pages, int page, const int *table, int n_slots, int max_pages,
+                                   const int *lens, const int *rows, void *out, void *workspace,
+                                   size_t workspace_bytes, path_stream_t stream);
+
+/*
+ * The same for sequences that all continue one prefix of prefix_len >= 1 rows, whose
+ * attention is computed once for the whole batch. The prefix's pages (prefix_table:
+ * ceil(prefix_len / page) pages of the same pool, e.g. the prefix slot's row of table)
+ * are only read: its keys p_j and gate biases g_j stay as they were when it ended.
+ * Instead each slot carries
+ *   state   [n_slots, H, d, d] fp32, G = H_t ... H_{P+1}, the product of the Householder
+ *           factors since the prefix ended (row-major; identity at its end),
+ *   g_state [n_slots, H] fp32, the sum of log_f since then (with the gate; 0 at its end),
+ * and a step computes G <- (I - beta w w^T) G, g_state <- g_state + log_f, and
+ *   out = softmax over {scale * (G^T q)^T p_j + g_state + g_j} and the slot's own rows,
+ * since q^T (G p_j) = (G^T q)^T p_j. path_state_copy sets a slot to the identity.
+ * The own rows, lens, errors and everything else as path_decode_step_paged; an
+ * out-of-range page of the prefix makes every row NaN. The prefix's pages must not be
+ * among the pages of the batch's slots.
+ */
+path_status path_decode_step_shared(const void *q, const void *k_new, const void *v_new, const void *w,
+                                    const float *beta, const float *log_f, float scale, int B, int H,
+                                    int d, path_dtype dt, void *k_pages, void *v_pages, float *g_pages,
+                                    int n_pages, int page, const int *table, int n_slots, int max_pages,
+                                    const int *lens, const int *rows, const int *prefix_table,
+                                    int prefix_len, float *state, float *g_state, void *out,
+                                    void *workspace, size_t workspace_bytes, path_stream_t stream);
+
+/*
+ * Page tables, on the device. Free pages are given in ascending order, to the rows in the
+ * order of their list, so results depend on the arguments alone. info [4] int32 on the
+ * device receives: status (0, or PATH_ERR_PAGE: the call changed no table), moves
+ * listed, pages in use, pages given.
+ *
+ * path_pages_reserve: gives slot rows[i] the pages it still lacks to hold tokens[i] rows.
+ * PATH_ERR_PAGE if there are too few free pages, tokens[i] is negative or above
+ * max_pages * page, a slot is out of range or stands twice.
+ *
+ * path_pages_fork: children[i], a slot that holds no pages, gets as many pages as
+ * parents[i]'s lens rows fill, and its lens; moves [max_moves, 2] int32 lists the pages to
+ * copy (source, destination), for path_pages_copy to run on each layer's pool. A negative
+ * parent makes an empty child (a sequence that starts at the prefix's end).
+ * max_moves >= min(n * max_pages, n_pages). Errors as reserve; also if a child holds pages.
+ *
+ * path_pages_free: the slots' pages become free, held and lens 0, their entries -1. No info;
+ * out-of-range slots are skipped.
+ *
+ * path_pages_compact: moves the pages in use to the front of the pool, [0, pages in use):
+ * each used page behind them, in ascending order, to the lowest free page; tables follow at
+ * once, the data with path_pages_copy. max_moves >= n_pages / 2. PATH_ERR_PAGE if an owner
+ * and its table entry disagree.
+ *
+ * path_pages_copy: copies the pages that a fork or compaction listed (info[1] of them, at
+ * most max_moves) in one pool, keys, values and (g_pages not NULL) gate biases. A move out
+ * of range is skipped and info[0] set to PATH_ERR_PAGE. No destination may be a source.
+ */
+path_status path_pages_reserve(int *table, int *held, int *owner, int n_slots, int max_pages, int n_pages,
+                               int page, const int *rows, const int *tokens, int n, int *info,
+                               path_stream_t stream);
+path_status path_pages_fork(int *table, int *held, int *lens, int *owner, int n_slots, int max_pages,
+                            int n_pages, int page, const int *parents, const int *children, int n,
+                            int *moves, int max_moves, int *info, path_stream_t stream);
+path_status path_pages_free(int *table, int *held, int *lens, int *owner, int n_slots, int max_pages,
+                            int n_pages, const int *rows, int n, path_stream_t stream);
+path_status path_pages_compact(int *table, const int *held, int *owner, int n_slots, int max_pages,
+                               int n_pages, int *moves, int max_moves, int *info, path_stream_t stream);
+path_status path_pages_copy(const int *moves, int max_moves, int *info, void *k_pages, void *v_pages,
+                            float *g_pages, int n_pages, int H, int page, int d, path_dtype dt,
+                            path_stream_t stream);
+
+/*
+ * Writes the first tokens[b] rows of a contiguous cache (k_cache, v_cache
+ * [B,H,capacity,d], g_cache [B,H,capacity]: what path_attn_prefill leaves) into the pages
+ * of slot rows[b] (b if rows is NULL), from its row 0; g_cache and g_pages go together.
+ * Rows behind tokens[b] keep what they held. A slot, count (0 to capacity and
+ * max_pages * page) or page out of range is skipped and sets info[0] to PATH_ERR_PAGE if
+ * info is not NULL (it is not cleared otherwise). lens is the caller's.
+ */
+path_status path_pages_store(const void *k_cache, const void *v_cache, const float *g_cache, int B, int H,
+                             int d, int capacity, path_dtype dt, void *k_pages, void *v_pages,
+                             float *g_pages, int n_pages, int page, const int *table, int n_slots,
+                             int max_pages, const int *rows, const int *tokens, int *info,
+                             path_stream_t stream);
+
+/*
+ * state (and g_state, if not NULL) of slot parents[i] into slot children[i]; a negative
+ * parent stands for the prefix's end: the identity, and 0. Out-of-range slots are skipped.
+ * No child may be a parent of another child.
+ */
+path_status path_state_copy(float *state, float *g_state, int n_slots, int H, int d, const int *parents,
+                            const int *children, int n, path_stream_t stream);
 
 /*
  * The w / beta prologue: the model-layer step that makes the attention's w and

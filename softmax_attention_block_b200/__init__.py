@@ -25,6 +25,12 @@ Entry points (same names as the C ABI):
 - the w / beta prologue: ``path_wbeta_fwd(x, A, Bw, f, U, b, H, beta_max=2.0) -> (w, beta)``,
   ``path_wbeta_bwd(x, A, Bw, f, U, b, H, dw, dbeta, beta_max=2.0) -> dict``,
   ``path_wbeta_workspace_bytes``
+- the paged decode cache (a pool of pages, and tables on the device):
+  ``path_decode_step_paged(q, k_new, v_new, w, beta, k_pages, v_pages, table, lens, rows=None)
+  -> out``, ``path_decode_step_shared(..., prefix_table, prefix_len, state, rows=None) -> out``
+  (a batch behind one shared prefix), ``path_pages_reserve``, ``path_pages_fork``,
+  ``path_pages_free``, ``path_pages_compact``, ``path_pages_copy``, ``path_pages_store``,
+  ``path_state_copy``, ``path_decode_paged_workspace_bytes``
 - test hook: ``path_test_withhold_kv_load(on)`` (makes the forward's bounded waits give up)
 """
 from __future__ import annotations
@@ -38,6 +44,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libpath_attn.so")
 
 PATH_F32, PATH_BF16, PATH_BF16_F32OUT = 0, 1, 2
+PATH_ERR_PAGE = 6
 _DT = {torch.float32: PATH_F32, torch.bfloat16: PATH_BF16}
 
 
@@ -101,6 +108,23 @@ def lib() -> ctypes.CDLL:
                                      fp, fp, fp, fp, ctypes.c_uint, vp, sz, vp]
         L.path_wbeta_fwd.restype = i
         L.path_wbeta_bwd.restype = i
+        L.path_decode_paged_workspace_bytes.argtypes = [i] * 7
+        L.path_decode_paged_workspace_bytes.restype = sz
+        step = [vp, vp, vp, vp, fp, fp, f, i, i, i, i, vp, vp, fp, i, i, vp, i, i, vp, vp]
+        L.path_decode_step_paged.argtypes = [*step, vp, vp, sz, vp]
+        L.path_decode_step_shared.argtypes = [*step, vp, i, fp, fp, vp, vp, sz, vp]
+        L.path_pages_reserve.argtypes = [vp, vp, vp, i, i, i, i, vp, vp, i, vp, vp]
+        L.path_pages_fork.argtypes = [vp, vp, vp, vp, i, i, i, i, vp, vp, i, vp, i, vp, vp]
+        L.path_pages_free.argtypes = [vp, vp, vp, vp, i, i, i, vp, i, vp]
+        L.path_pages_compact.argtypes = [vp, vp, vp, i, i, i, vp, i, vp, vp]
+        L.path_pages_copy.argtypes = [vp, i, vp, vp, vp, fp, i, i, i, i, i, vp]
+        L.path_pages_store.argtypes = [vp, vp, fp, i, i, i, i, i, vp, vp, fp, i, i, vp, i, i, vp, vp,
+                                       vp, vp]
+        L.path_state_copy.argtypes = [fp, fp, i, i, i, vp, vp, i, vp]
+        for fn in (L.path_decode_step_paged, L.path_decode_step_shared, L.path_pages_reserve,
+                   L.path_pages_fork, L.path_pages_free, L.path_pages_compact, L.path_pages_copy,
+                   L.path_pages_store, L.path_state_copy):
+            fn.restype = i
         L.path_test_withhold_kv_load.argtypes = [i]
         L.path_test_withhold_kv_load.restype = i
         L.path_kernel_launch_count.restype = ctypes.c_ulonglong
@@ -339,7 +363,9 @@ def path_decode_step_noalloc(q, k_new, v_new, w, beta, k_cache, v_cache, n_cache
 
 def path_attn_wait_status(workspace) -> int:
     """Waits for the current stream, then returns 0, or PATH_ERR_TIMEOUT (5) if the last
-    path_attn_fwd / path_attn_bwd that used `workspace` had a bounded wait give up."""
+    path_attn_fwd / path_attn_bwd that used `workspace` had a bounded wait give up, or
+    PATH_ERR_PAGE (6) if the last paged decode step that used it met a page, slot or length
+    out of range."""
     _check_dev(workspace)
     return int(lib().path_attn_wait_status(_ptr(workspace), _stream()))
 
@@ -409,6 +435,244 @@ def path_test_withhold_kv_load(on: bool) -> None:
     st = lib().path_test_withhold_kv_load(1 if on else 0)
     if st:
         raise PathError(st, "path_test_withhold_kv_load")
+
+
+# ---------------------------------------------------------------- the paged decode cache
+def _expect_pool(k_pages, v_pages, g_pages):
+    if k_pages.dim() != 4 or k_pages.dtype not in _DT:
+        raise ValueError("k_pages must be [n_pages,H,page,d], float32 or bfloat16")
+    _expect("v_pages", v_pages, k_pages.shape, k_pages.dtype)
+    _expect("g_pages", g_pages, k_pages.shape[:3], torch.float32)
+    return k_pages.shape
+
+
+def _expect_table(table, **per_slot):
+    if table.dim() != 2:
+        raise ValueError("table must be [n_slots,max_pages]")
+    _expect("table", table, table.shape, torch.int32)
+    for n, t in per_slot.items():
+        _expect(n, t, table.shape[:1], torch.int32)
+    return table.shape
+
+
+def _expect_owner(owner):
+    if owner.dim() != 1:
+        raise ValueError("owner must be [n_pages]")
+    _expect("owner", owner, owner.shape, torch.int32)
+    return owner.shape[0]
+
+
+def _expect_list(**lists):
+    """int32 lists of one length; returns it."""
+    n = None
+    for name, t in lists.items():
+        if t.dim() != 1:
+            raise ValueError(f"{name}: must have one dimension")
+        n = t.shape[0] if n is None else n
+        _expect(name, t, (n,), torch.int32)
+    return n
+
+
+def _moves(moves, most, device):
+    """The caller's list of moves, or a new one of `most` pairs, and its length."""
+    if moves is None:
+        moves = torch.empty((max(most, 1), 2), dtype=torch.int32, device=device)
+    if moves.dim() != 2:
+        raise ValueError("moves must be [max_moves,2]")
+    _expect("moves", moves, (moves.shape[0], 2), torch.int32)
+    return moves, moves.shape[0]
+
+
+def _info(info, device):
+    if info is None:
+        info = torch.zeros(4, dtype=torch.int32, device=device)
+    _expect("info", info, (4,), torch.int32)
+    return info
+
+
+def path_decode_paged_workspace_bytes(B, H, max_pages, page, d, dtype, prefix_len=0) -> int:
+    return int(lib().path_decode_paged_workspace_bytes(B, H, max_pages, page, d, _DT[dtype],
+                                                       int(prefix_len)))
+
+
+def _step_paged(where, q, k_new, v_new, w, beta, k_pages, v_pages, table, lens, rows, scale, log_f,
+                g_pages, out, workspace, prefix=None):
+    n_pages, H, page, d = _expect_pool(k_pages, v_pages, g_pages)
+    if q.dim() != 3:
+        raise ValueError("q must be [B,H,d]")
+    B, dtype = q.shape[0], k_pages.dtype
+    if out is None:  # an idle row's output is not written
+        out = torch.empty_like(q) if rows is None else torch.zeros_like(q)
+    if (log_f is None) != (g_pages is None):
+        raise ValueError("log_f and g_pages go together")
+    for n, t in (("q", q), ("k_new", k_new), ("v_new", v_new), ("w", w), ("out", out)):
+        _expect(n, t, (B, H, d), dtype)
+    _expect("beta", beta, (B, H), torch.float32)
+    _expect("log_f", log_f, (B, H), torch.float32)
+    n_slots, max_pages = _expect_table(table, lens=lens)
+    _expect("rows", rows, (B,), torch.int32)
+    prefix_len, more, extra = 0, (), ()
+    if prefix is not None:
+        prefix_table, prefix_len, state, g_state = prefix
+        prefix_len = int(prefix_len)
+        _expect_list(prefix_table=prefix_table)
+        if prefix_len > prefix_table.shape[0] * page:
+            raise ValueError(f"prefix_table: {prefix_table.shape[0]} pages of {page} rows do not "
+                             f"hold prefix_len={prefix_len}")
+        if (log_f is None) != (g_state is None):
+            raise ValueError("log_f and g_state go together")
+        _expect("state", state, (n_slots, H, d, d), torch.float32)
+        _expect("g_state", g_state, (n_slots, H), torch.float32)
+        more = (prefix_table, state, g_state)
+        extra = (_ptr(prefix_table), prefix_len, _ptr(state), _ptr(g_state))
+    _check_dev(q, k_new, v_new, w, beta, log_f, k_pages, v_pages, g_pages, table, lens, rows, out,
+               workspace, *more)
+    nbytes = path_decode_paged_workspace_bytes(B, H, max_pages, page, d, dtype, prefix_len)
+    ws = _workspace(nbytes, q.device, workspace)
+    st = getattr(lib(), where)(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(w), _ptr(beta), _ptr(log_f),
+                               _scale(scale, d), B, H, d, _DT[dtype], _ptr(k_pages), _ptr(v_pages),
+                               _ptr(g_pages), n_pages, page, _ptr(table), n_slots, max_pages,
+                               _ptr(lens), _ptr(rows), *extra, _ptr(out), _ptr(ws), nbytes,
+                               _stream())
+    if st:
+        raise PathError(st, where)
+    return out
+
+
+def path_decode_step_paged(q, k_new, v_new, w, beta, k_pages, v_pages, table, lens, rows=None,
+                           scale=None, log_f=None, g_pages=None, out=None, workspace=None):
+    """One decode step of a ragged batch over paged caches. q, k_new, v_new, w: [B,H,d]; beta
+    (and log_f): [B,H] fp32; k_pages, v_pages: [n_pages,H,page,d] (g_pages [n_pages,H,page] fp32
+    with log_f), updated in place; table [n_slots,max_pages] and lens [n_slots] int32; rows [B]
+    int32: the slot of each batch row (default: its own number; negative: idle, its row of out is
+    left as it was). lens is not advanced. Returns out [B,H,d]."""
+    return _step_paged("path_decode_step_paged", q, k_new, v_new, w, beta, k_pages, v_pages, table,
+                       lens, rows, scale, log_f, g_pages, out, workspace)
+
+
+def path_decode_step_shared(q, k_new, v_new, w, beta, k_pages, v_pages, table, lens, prefix_table,
+                            prefix_len, state, rows=None, scale=None, log_f=None, g_pages=None,
+                            g_state=None, out=None, workspace=None):
+    """path_decode_step_paged for sequences that continue one prefix: prefix_len rows in the pages
+    prefix_table (int32) of the same pool, which stay as they are. state [n_slots,H,d,d] fp32 (and
+    g_state [n_slots,H] with the gate) holds each slot's product of Householder factors (sum of
+    log_f) since the prefix ended, updated in place; path_state_copy starts a slot."""
+    return _step_paged("path_decode_step_shared", q, k_new, v_new, w, beta, k_pages, v_pages, table,
+                       lens, rows, scale, log_f, g_pages, out, workspace,
+                       (prefix_table, prefix_len, state, g_state))
+
+
+def path_pages_reserve(table, held, owner, page, rows, tokens, info=None):
+    """Gives slot rows[i] the free pages it lacks to hold tokens[i] rows, or changes nothing and
+    reports PATH_ERR_PAGE. Returns info [4] int32 on the device: status, moves, pages in use,
+    pages given."""
+    n_slots, max_pages = _expect_table(table, held=held)
+    n_pages, n = _expect_owner(owner), _expect_list(rows=rows, tokens=tokens)
+    info = _info(info, table.device)
+    _check_dev(table, held, owner, rows, tokens, info)
+    st = lib().path_pages_reserve(_ptr(table), _ptr(held), _ptr(owner), n_slots, max_pages, n_pages,
+                                  int(page), _ptr(rows), _ptr(tokens), n, _ptr(info), _stream())
+    if st:
+        raise PathError(st, "path_pages_reserve")
+    return info
+
+
+def path_pages_fork(table, held, lens, owner, page, parents, children, moves=None, info=None):
+    """Gives each child, a slot without pages, pages for its parent's rows and the parent's length
+    (negative parent: an empty child), and lists the pages to copy. Returns (moves [max_moves,2],
+    info [4]) on the device, for path_pages_copy on each layer's pool."""
+    n_slots, max_pages = _expect_table(table, held=held, lens=lens)
+    n_pages, n = _expect_owner(owner), _expect_list(parents=parents, children=children)
+    moves, most = _moves(moves, min(n * max_pages, n_pages), table.device)
+    info = _info(info, table.device)
+    _check_dev(table, held, lens, owner, parents, children, moves, info)
+    st = lib().path_pages_fork(_ptr(table), _ptr(held), _ptr(lens), _ptr(owner), n_slots, max_pages,
+                               n_pages, int(page), _ptr(parents), _ptr(children), n, _ptr(moves),
+                               most, _ptr(info), _stream())
+    if st:
+        raise PathError(st, "path_pages_fork")
+    return moves, info
+
+
+def path_pages_free(table, held, lens, owner, rows):
+    """Frees the slots' pages: their entries and owners become -1, held and lens 0."""
+    n_slots, max_pages = _expect_table(table, held=held, lens=lens)
+    n_pages, n = _expect_owner(owner), _expect_list(rows=rows)
+    _check_dev(table, held, lens, owner, rows)
+    st = lib().path_pages_free(_ptr(table), _ptr(held), _ptr(lens), _ptr(owner), n_slots, max_pages,
+                               n_pages, _ptr(rows), n, _stream())
+    if st:
+        raise PathError(st, "path_pages_free")
+
+
+def path_pages_compact(table, held, owner, moves=None, info=None):
+    """Renumbers the pages in use to the front of the pool. Returns (moves, info) as
+    path_pages_fork, for path_pages_copy on each layer's pool."""
+    n_slots, max_pages = _expect_table(table, held=held)
+    n_pages = _expect_owner(owner)
+    moves, most = _moves(moves, n_pages // 2, table.device)
+    info = _info(info, table.device)
+    _check_dev(table, held, owner, moves, info)
+    st = lib().path_pages_compact(_ptr(table), _ptr(held), _ptr(owner), n_slots, max_pages, n_pages,
+                                  _ptr(moves), most, _ptr(info), _stream())
+    if st:
+        raise PathError(st, "path_pages_compact")
+    return moves, info
+
+
+def path_pages_copy(moves, info, k_pages, v_pages, g_pages=None):
+    """Copies the pages that path_pages_fork or path_pages_compact listed in one layer's pool."""
+    n_pages, H, page, d = _expect_pool(k_pages, v_pages, g_pages)
+    moves, most = _moves(moves, 0, k_pages.device)
+    _expect("info", info, (4,), torch.int32)
+    _check_dev(moves, info, k_pages, v_pages, g_pages)
+    st = lib().path_pages_copy(_ptr(moves), most, _ptr(info), _ptr(k_pages), _ptr(v_pages),
+                               _ptr(g_pages), n_pages, H, page, d, _DT[k_pages.dtype], _stream())
+    if st:
+        raise PathError(st, "path_pages_copy")
+
+
+def path_pages_store(k_cache, v_cache, k_pages, v_pages, table, rows, tokens, g_cache=None,
+                     g_pages=None, info=None):
+    """Writes rows 0..tokens[b]-1 of the contiguous caches [B,H,capacity,d] (path_attn_prefill's)
+    into the pages of slot rows[b] (None: b). info [4] int32, if given, reports PATH_ERR_PAGE in
+    info[0]."""
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must be [B,H,capacity,d]")
+    n_pages, H, page, d = _expect_pool(k_pages, v_pages, g_pages)
+    if (g_cache is None) != (g_pages is None):
+        raise ValueError("g_cache and g_pages go together")
+    B, _, capacity, _ = k_cache.shape
+    for n, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _expect(n, t, (B, H, capacity, d), k_pages.dtype)
+    _expect("g_cache", g_cache, (B, H, capacity), torch.float32)
+    n_slots, max_pages = _expect_table(table)
+    _expect("rows", rows, (B,), torch.int32)
+    _expect("tokens", tokens, (B,), torch.int32)
+    _expect("info", info, (4,), torch.int32)
+    _check_dev(k_cache, v_cache, g_cache, k_pages, v_pages, g_pages, table, rows, tokens, info)
+    st = lib().path_pages_store(_ptr(k_cache), _ptr(v_cache), _ptr(g_cache), B, H, d, capacity,
+                                _DT[k_pages.dtype], _ptr(k_pages), _ptr(v_pages), _ptr(g_pages),
+                                n_pages, page, _ptr(table), n_slots, max_pages, _ptr(rows),
+                                _ptr(tokens), _ptr(info), _stream())
+    if st:
+        raise PathError(st, "path_pages_store")
+
+
+def path_state_copy(state, parents, children, g_state=None):
+    """state [n_slots,H,d,d] (and g_state [n_slots,H]) of slot parents[i] into slot children[i];
+    a negative parent stands for the prefix's end (identity, 0)."""
+    if state.dim() != 4:
+        raise ValueError("state must be [n_slots,H,d,d]")
+    n_slots, H, d, _ = state.shape
+    _expect("state", state, (n_slots, H, d, d), torch.float32)
+    _expect("g_state", g_state, (n_slots, H), torch.float32)
+    n = _expect_list(parents=parents, children=children)
+    _check_dev(state, g_state, parents, children)
+    st = lib().path_state_copy(_ptr(state), _ptr(g_state), n_slots, H, d, _ptr(parents),
+                               _ptr(children), n, _stream())
+    if st:
+        raise PathError(st, "path_state_copy")
 
 
 # ---------------------------------------------------------------- the w / beta prologue

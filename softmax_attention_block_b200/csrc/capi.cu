@@ -4,6 +4,7 @@
 
 #include "attn.cuh"
 #include "attn_tc.cuh"
+#include "paged.cuh"
 #include "prep.cuh"
 #include "runtime.cuh"
 
@@ -240,6 +241,7 @@ const char *path_status_string(path_status s)
     case PATH_ERR_WORKSPACE: return "workspace missing or too small";
     case PATH_ERR_CUDA: return "CUDA launch failed";
     case PATH_ERR_TIMEOUT: return "device-side wait timed out";
+    case PATH_ERR_PAGE: return "paged cache: page, slot or length out of range, or no page free";
     }
     return "unknown status";
 }
@@ -374,6 +376,7 @@ path_status path_attn_wait_status(const void *workspace, path_stream_t stream)
         cudaStreamSynchronize(st) != cudaSuccess)
         return PATH_ERR_CUDA;
     if (code == ERR_UT_NOT_SAVED) return PATH_ERR_WORKSPACE;
+    if (code == ERR_PAGE) return PATH_ERR_PAGE;
     return code ? PATH_ERR_TIMEOUT : PATH_OK;
 }
 

@@ -1,0 +1,319 @@
+// Decode attention of a batch to one shared prefix, computed once for all.
+//
+// The keys of a prefix that many sequences continue cannot be updated in place:
+// each sequence has its own factors. But the update is linear, and with
+// G_t = H_t ... H_{P+1} (P the prefix's last position)
+//   q_t^T (H_t ... H_{P+1}) k_j^{(P)} = (G_t^T q_t)^T k_j^{(P)}
+// (from the logit equation, gist.science section 2), so the prefix's keys stay as
+// they were when it ended and the query is turned back instead. A sequence
+// carries G per head, d x d fp32, and one step costs it a rank-1 update:
+//   y = G^T w;  G <- G - beta w y^T;  G_new^T q = G^T q - beta (q.w) y.
+#include "paged.cuh"
+#include "rowvec.cuh"
+#include "runtime.cuh"
+#include "tc.cuh"
+
+namespace path {
+
+namespace {
+
+constexpr int NT = 256;
+constexpr float LOG2E = 1.4426950408889634f;
+
+// One (batch row, head): G read once and written once, bound by HBM (8 d^2
+// bytes). A thread keeps D * D / 1024 vectors of four columns in registers.
+template <typename T, int D>
+__global__ void __launch_bounds__(NT) turn_kernel(PagedStep a, PagedScratch s, int q_rows)
+{
+    constexpr int CG = D / 4;       // groups of four columns
+    constexpr int RG = NT / CG;     // rows of a pass
+    constexpr int R = D / RG;       // rows a thread keeps
+    __shared__ float sw[D], sq[D];
+    __shared__ float4 red[2][RG][CG];
+    const int u = blockIdx.x, b = u / a.H, h = u % a.H, tid = threadIdx.x;
+    const int cg = tid % CG, rg = tid / CG;
+    const int slot = slot_of(a.c, b);
+    float *qt = s.qt + ((long long)h * q_rows + b) * D;
+    if (slot < 0 || length_of(a.c, slot) < 0) {  // idle or invalid: a query of zeros, not read
+        if (tid < D) qt[tid] = 0.f;
+        if (tid == 0) s.qg[(long long)h * q_rows + b] = 0.f;
+        return;
+    }
+    if (tid < D) {
+        sw[tid] = to_f(static_cast<const T *>(a.w)[(long long)u * D + tid]);
+        sq[tid] = to_f(static_cast<const T *>(a.q)[(long long)u * D + tid]);
+    }
+    float4 *G = reinterpret_cast<float4 *>(a.state) + ((long long)slot * a.H + h) * (D * CG);
+    float4 x[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) x[i] = G[(i * RG + rg) * CG + cg];
+    __syncthreads();
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f), z = y;
+    float qw = 0.f;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const float w = sw[i * RG + rg], q = sq[i * RG + rg];
+        y.x = fmaf(w, x[i].x, y.x);
+        y.y = fmaf(w, x[i].y, y.y);
+        y.z = fmaf(w, x[i].z, y.z);
+        y.w = fmaf(w, x[i].w, y.w);
+        z.x = fmaf(q, x[i].x, z.x);
+        z.y = fmaf(q, x[i].y, z.y);
+        z.z = fmaf(q, x[i].z, z.z);
+        z.w = fmaf(q, x[i].w, z.w);
+    }
+    red[0][rg][cg] = y;
+    red[1][rg][cg] = z;
+    for (int i = 0; i < D; ++i) qw = fmaf(sq[i], sw[i], qw);
+    __syncthreads();
+    y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < RG; ++i) {
+        const float4 t = red[0][i][cg];
+        y.x += t.x;
+        y.y += t.y;
+        y.z += t.z;
+        y.w += t.w;
+    }
+    const float beta = a.beta[u];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const float f = -beta * sw[i * RG + rg];
+        x[i].x = fmaf(f, y.x, x[i].x);
+        x[i].y = fmaf(f, y.y, x[i].y);
+        x[i].z = fmaf(f, y.z, x[i].z);
+        x[i].w = fmaf(f, y.w, x[i].w);
+        G[(i * RG + rg) * CG + cg] = x[i];
+    }
+    if (rg == 0) {
+        z = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < RG; ++i) {
+            const float4 t = red[1][i][cg];
+            z.x += t.x;
+            z.y += t.y;
+            z.z += t.z;
+            z.w += t.w;
+        }
+        const float f = -beta * qw;
+        reinterpret_cast<float4 *>(qt)[cg] =
+            make_float4(fmaf(f, y.x, z.x), fmaf(f, y.y, z.y), fmaf(f, y.z, z.z), fmaf(f, y.w, z.w));
+    }
+    if (tid == 0) {
+        float g = 0.f;
+        if (a.g_state) {
+            float *gs = a.g_state + (long long)slot * a.H + h;
+            g = *gs + a.log_f[u];
+            *gs = g;
+        }
+        s.qg[(long long)h * q_rows + b] = g * LOG2E;
+    }
+}
+
+// fp32 arithmetic on CUDA cores: 32 queries by 64 keys a tile, one pass over
+// the keys with a running maximum and sum. Thread (ty, tx) holds queries
+// 2 ty, 2 ty + 1 against keys tx + 16 i, then dims 4 tx + 64 i of their output.
+constexpr int QT = 32, KT = 64;
+
+template <int D>
+struct SimtCfg {
+    static constexpr int LD = D + 4, LP = KT + 4;
+    static constexpr int Q = 0, K = Q + QT * LD, V = K + KT * LD, P = V + KT * D, G = P + QT * LP;
+    static constexpr int SMEM = (G + KT) * 4;
+};
+
+// Rows of a key tile into shared memory as fp32; rows past the prefix are zero.
+template <typename T, int D>
+__device__ __forceinline__ bool load_tile(const void *pool, const PagedStep &a, int h, int key0, float *dst, int ld)
+{
+    constexpr int V = Vec<T>::N, LPR = D / V;
+    bool bad = false;
+    for (int i = threadIdx.x; i < KT * LPR; i += NT) {
+        const int r = i / LPR, x = i % LPR, key = key0 + r;
+        uint4 u = make_uint4(0u, 0u, 0u, 0u);
+        if (key < a.prefix_len) {
+            const int p = a.prefix_table[key >> a.c.page_log2];
+            if (p >= 0 && p < a.c.n_pages)
+                u = static_cast<const uint4 *>(pool)[((((long long)p * a.H + h) << a.c.page_log2) +
+                                                      (key & ((1 << a.c.page_log2) - 1))) * LPR + x];
+            else
+                bad = true;
+        }
+        float f[V];
+        unpack<T>(u, f);
+#pragma unroll
+        for (int e = 0; e < V; e += 4)
+            *reinterpret_cast<float4 *>(dst + r * ld + x * V + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+    }
+    return bad;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(NT) prefix_simt_kernel(PagedStep a, PagedScratch s, PagedPlan p)
+{
+    using C = SimtCfg<D>;
+    constexpr int LD = C::LD, LP = C::LP, DV = D / 64;  // float4 columns a thread accumulates
+    extern __shared__ float sm[];
+    float *sQ = sm + C::Q, *sK = sm + C::K, *sV = sm + C::V, *sP = sm + C::P, *sG = sm + C::G;
+    const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
+    const int q_rows = p.q_tiles * QT;
+    const float scale2 = a.scale * LOG2E;
+    const long long total = (long long)p.pre_units * p.key_tiles;
+    const long long t0 = total * blockIdx.x / gridDim.x, t1 = total * (blockIdx.x + 1) / gridDim.x;
+    for (long long t = t0; t < t1;) {
+        const int u = (int)(t / p.key_tiles), kb = (int)(t % p.key_tiles);
+        const int ke = (int)min((long long)p.key_tiles, kb + (t1 - t));
+        const int qtile = u % p.q_tiles, h = u / p.q_tiles;
+        for (int i = tid; i < QT * D; i += NT) {
+            const int r = i / D, e = i % D, b = qtile * QT + r;
+            sQ[r * LD + e] = b < a.B ? s.qt[((long long)h * q_rows + b) * D + e] : 0.f;
+        }
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+        float4 acc[2][DV];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int e = 0; e < DV; ++e) acc[i][e] = make_float4(0.f, 0.f, 0.f, 0.f);
+        bool bad = false;
+        for (int kt = kb; kt < ke; ++kt) {
+            const int key0 = kt * KT;
+            __syncthreads();  // the former tile is done with
+            bad |= load_tile<T, D>(a.c.k, a, h, key0, sK, LD);
+            bad |= load_tile<T, D>(a.c.v, a, h, key0, sV, D);
+            if (tid < KT) {
+                const int key = key0 + tid;
+                float g = -INFINITY;  // a key past the prefix
+                if (key < a.prefix_len) {
+                    const int pg = a.prefix_table[key >> a.c.page_log2];
+                    g = 0.f;
+                    if (a.c.g && pg >= 0 && pg < a.c.n_pages)
+                        g = a.c.g[(((long long)pg * a.H + h) << a.c.page_log2) + (key & ((1 << a.c.page_log2) - 1))] * LOG2E;
+                }
+                sG[tid] = g;
+            }
+            __syncthreads();
+            float z[2][4] = {};
+#pragma unroll 4
+            for (int e = 0; e < D; e += 4) {
+                const float4 q0 = *reinterpret_cast<const float4 *>(sQ + (2 * ty) * LD + e);
+                const float4 q1 = *reinterpret_cast<const float4 *>(sQ + (2 * ty + 1) * LD + e);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float4 k = *reinterpret_cast<const float4 *>(sK + (tx + 16 * j) * LD + e);
+                    z[0][j] = fmaf(q0.x, k.x, fmaf(q0.y, k.y, fmaf(q0.z, k.z, fmaf(q0.w, k.w, z[0][j]))));
+                    z[1][j] = fmaf(q1.x, k.x, fmaf(q1.y, k.y, fmaf(q1.z, k.z, fmaf(q1.w, k.w, z[1][j]))));
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float mx = m[i];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float g = sG[tx + 16 * j];
+                    z[i][j] = key0 + tx + 16 * j < a.prefix_len ? fmaf(z[i][j], scale2, g) : -INFINITY;
+                    mx = fmaxf(mx, z[i][j]);
+                }
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                const float base = mx == -INFINITY ? 0.f : mx;  // a row without a weight so far
+                const float corr = tc::ex2(m[i] - base);
+                float sum = 0.f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float w = tc::ex2(z[i][j] - base);
+                    sP[(2 * ty + i) * LP + tx + 16 * j] = w;
+                    sum += w;
+                }
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                l[i] = fmaf(l[i], corr, sum);
+                m[i] = mx;
+#pragma unroll
+                for (int e = 0; e < DV; ++e) {
+                    acc[i][e].x *= corr;
+                    acc[i][e].y *= corr;
+                    acc[i][e].z *= corr;
+                    acc[i][e].w *= corr;
+                }
+            }
+            __syncwarp();  // a warp's rows of P are its own
+#pragma unroll 4
+            for (int j = 0; j < KT; ++j) {
+                const float p0 = sP[(2 * ty) * LP + j], p1 = sP[(2 * ty + 1) * LP + j];
+#pragma unroll
+                for (int e = 0; e < DV; ++e) {
+                    const float4 v = *reinterpret_cast<const float4 *>(sV + j * D + 4 * tx + 64 * e);
+                    acc[0][e].x = fmaf(p0, v.x, acc[0][e].x);
+                    acc[0][e].y = fmaf(p0, v.y, acc[0][e].y);
+                    acc[0][e].z = fmaf(p0, v.z, acc[0][e].z);
+                    acc[0][e].w = fmaf(p0, v.w, acc[0][e].w);
+                    acc[1][e].x = fmaf(p1, v.x, acc[1][e].x);
+                    acc[1][e].y = fmaf(p1, v.y, acc[1][e].y);
+                    acc[1][e].z = fmaf(p1, v.z, acc[1][e].z);
+                    acc[1][e].w = fmaf(p1, v.w, acc[1][e].w);
+                }
+            }
+        }
+        const long long piece = (long long)blockIdx.x + u;
+        const bool any_bad = __syncthreads_or(bad);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = 2 * ty + i, b = qtile * QT + r;
+            if (b < a.B) {
+                float *o = s.pre + (piece * QT + r) * D;
+#pragma unroll
+                for (int e = 0; e < DV; ++e) *reinterpret_cast<float4 *>(o + 4 * tx + 64 * e) = acc[i][e];
+                if (tx == 0) {
+                    // the gate since the prefix's end weighs every key of it alike; where it
+                    // leaves nothing (log f = -inf), neither the sum nor the values count
+                    const float M = m[i] + s.qg[(long long)h * q_rows + b];
+                    s.pre_ml[piece * 2 * QT + r] = M;
+                    s.pre_ml[piece * 2 * QT + QT + r] = M == -INFINITY && !isnan(l[i]) ? 0.f : l[i];
+                }
+            }
+        }
+        if (tid == 0) s.pre_flag[piece] = any_bad;
+        t += ke - kb;
+    }
+}
+
+template <typename T, int D>
+cudaError_t run_simt(const PagedStep &a, const PagedPlan &p, const PagedScratch &s, cudaStream_t st)
+{
+    auto k = prefix_simt_kernel<T, D>;
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SimtCfg<D>::SMEM);
+    if (e != cudaSuccess) return e;
+    k<<<p.pre_blocks, NT, SimtCfg<D>::SMEM, st>>>(a, s, p);
+    count_launches();
+    return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t run_turn(const PagedStep &a, const PagedPlan &p, const PagedScratch &s, cudaStream_t st)
+{
+    turn_kernel<T, D><<<a.B * a.H, NT, 0, st>>>(a, s, p.q_tiles * p.q_tile);
+    count_launches();
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t prefix_turn(const PagedStep &a, int dt, int d, const PagedPlan &p, const PagedScratch &s,
+                        cudaStream_t st)
+{
+    Stage stage("prefix_turn", st);
+    if (d == 64) return dt == F32 ? run_turn<float, 64>(a, p, s, st) : run_turn<bf16, 64>(a, p, s, st);
+    if (d == 128) return dt == F32 ? run_turn<float, 128>(a, p, s, st) : run_turn<bf16, 128>(a, p, s, st);
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t prefix_attn_simt(const PagedStep &a, int dt, int d, const PagedPlan &p,
+                             const PagedScratch &s, cudaStream_t st)
+{
+    Stage stage("prefix_attn", st);
+    if (d == 64) return dt == F32 ? run_simt<float, 64>(a, p, s, st) : run_simt<bf16, 64>(a, p, s, st);
+    if (d == 128) return dt == F32 ? run_simt<float, 128>(a, p, s, st) : run_simt<bf16, 128>(a, p, s, st);
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace path

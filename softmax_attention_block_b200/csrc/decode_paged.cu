@@ -15,26 +15,46 @@
 #include "runtime.cuh"
 #include "tc.cuh"
 
+#include <type_traits>
+
 namespace path {
 
 namespace {
 
-constexpr int NT = 256;
-constexpr int UNROLL = 8;
+constexpr int NT = 256, WARPS = NT / 32;
 constexpr float LOG2E = 1.4426950408889634f;
 
-// tiles of one head of batch row b (0: idle or invalid; the new token is a row)
+// A warp's granule: GR rows of K and V (and gate biases) of one head, always inside one page.
+// LPR lanes hold a row, 16 elements each as CPL 16-byte chunks; a pass takes 32 / LPR rows.
+template <typename T, int D>
+struct OwnCfg {
+    static constexpr int LPR = D / 16, RPP = 32 / LPR;
+    static constexpr int GR = own_granule(D, sizeof(T));
+    static constexpr int PASSES = GR / RPP;
+    static constexpr int CPL = sizeof(T);
+    static constexpr int ROW_CHUNKS = D * (int)sizeof(T) / 16;
+    static constexpr int TILE = GR * D * (int)sizeof(T);
+    static constexpr int STAGES = 24576 / (2 * TILE);
+    static constexpr int GATE = GR * 4;
+    // shared memory: the warps' rings, then the gate biases
+    static constexpr int RING = STAGES * 2 * TILE;
+    static constexpr int SMEM = WARPS * (RING + STAGES * GATE);
+    static_assert(GR % RPP == 0 && STAGES >= 2 && TILE % 128 == 0, "granule");
+};
+
+// Tiles (granules) of one head of batch row b (0: idle or invalid; the new token is a row).
+template <int GR>
 __device__ __forceinline__ int tiles_of(const PagedCache &c, int b)
 {
     const int slot = slot_of(c, b);
     if (slot < 0) return 0;
     const int n = length_of(c, slot);
-    return n < 0 ? 0 : n / OWN_TILE + 1;
+    return n < 0 ? 0 : n / GR + 1;
 }
 
 __device__ long long block_scan(long long x, long long *total)
 {
-    __shared__ long long s_w[NT / 32];
+    __shared__ long long s_w[WARPS];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     long long v = x;
 #pragma unroll
@@ -46,7 +66,7 @@ __device__ long long block_scan(long long x, long long *total)
     __syncthreads();
     long long before = 0, sum = 0;
 #pragma unroll
-    for (int i = 0; i < NT / 32; ++i) {
+    for (int i = 0; i < WARPS; ++i) {
         if (i < warp) before += s_w[i];
         sum += s_w[i];
     }
@@ -55,157 +75,433 @@ __device__ long long block_scan(long long x, long long *total)
     return before + v - x;
 }
 
-template <typename T, int D, bool GATE, bool SHARED>
-__global__ void __launch_bounds__(NT) decode_own_kernel(PagedStep a, PagedScratch s)
+// Pairs of fp32 numbers in one 64-bit register: one instruction for two products.
+typedef unsigned long long F2;
+__device__ __forceinline__ F2 f2(float lo, float hi)
 {
-    constexpr int V = Vec<T>::N;
-    constexpr int LPR = D / V;
-    constexpr int G = NT / LPR;
-    __shared__ float s_m[G], s_l[G];
-    __shared__ float s_acc[G][D];
-    __shared__ int s_row;
-    __shared__ long long s_cum;
-    const int tid = threadIdx.x, lane_in_row = tid % LPR, g = tid / LPR;
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void split(F2 x, float &lo, float &hi)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
+{
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b)
+{
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// One 16-byte chunk to pairs, N of them.
+template <typename T>
+__device__ __forceinline__ void to_pairs(const uint4 &u, F2 *x)
+{
+    float f[Vec<T>::N];
+    unpack<T>(u, f);
+#pragma unroll
+    for (int i = 0; i < Vec<T>::N / 2; ++i) x[i] = f2(f[2 * i], f[2 * i + 1]);
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 from_pairs(const F2 *x)
+{
+    float f[Vec<T>::N];
+#pragma unroll
+    for (int i = 0; i < Vec<T>::N / 2; ++i) split(x[i], f[2 * i], f[2 * i + 1]);
+    return pack<T>(f);
+}
+
+__device__ __forceinline__ float dot16(const F2 *a, const F2 *b)
+{
+    F2 s0 = mul2(a[0], b[0]), s1 = mul2(a[1], b[1]);
+#pragma unroll
+    for (int i = 2; i < 8; i += 2) {
+        s0 = fma2(a[i], b[i], s0);
+        s1 = fma2(a[i + 1], b[i + 1], s1);
+    }
+    float x0, y0, x1, y1;
+    split(s0, x0, y0);
+    split(s1, x1, y1);
+    return (x0 + y0) + (x1 + y1);
+}
+
+// Position in the list of all tiles: unit (b, h), tile j of its nt.
+struct Cursor {
+    int b, h, j, nt;
+    int slot, n;
+
+    template <int GR>
+    __device__ __forceinline__ void at_row(const PagedCache &c, int row)
+    {
+        b = row;
+        slot = slot_of(c, b);
+        n = slot < 0 ? -1 : length_of(c, slot);
+        nt = n < 0 ? 0 : n / GR + 1;
+    }
+};
+
+template <int GR>
+__device__ __forceinline__ void advance(const PagedStep &a, Cursor &c, long long left)
+{
+    if (++c.j < c.nt) return;
+    c.j = 0;
+    if (++c.h < a.H) return;
+    c.h = 0;
+    if (left <= 0) return;  // no tile follows in this share
+    do c.at_row<GR>(a.c, c.b + 1);
+    while (c.nt == 0);
+}
+
+// A unit's piece that a warp does not hold whole, for the block to put together.
+template <int D>
+struct Piece {
+    int u, flags;  // unit; bit 0: from its first tile, bit 1: to its last, bits 2..: errors
+    float m, l;
+    float acc[D];
+};
+enum { FIRST = 1, LAST = 2, BAD_PAGE = 4, GAVE_UP = 8 };
+
+template <typename T, int D, bool GATE, bool SHARED>
+__global__ void __launch_bounds__(NT, 1) decode_own_kernel(PagedStep a, PagedScratch s)
+{
+    using C = OwnCfg<T, D>;
+    constexpr int LPR = C::LPR, RPP = C::RPP, GR = C::GR, CPL = C::CPL, S = C::STAGES;
+    constexpr int VP = Vec<T>::N / 2;  // pairs of a chunk
+    extern __shared__ __align__(128) char smem[];
+    __shared__ uint64_t s_bar[WARPS][S];
+    __shared__ long long s_row[WARPS][S];  // first row of the stage's granule in the pool, or -1
+    __shared__ long long s_cum[NT];
+    __shared__ Piece<D> s_piece[WARPS][2];
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    const int lr = lane % LPR, grp = lane / LPR;
+    const int odd = LPR == 4 ? grp & 1 : 0;
     const PagedCache &c = a.c;
     const int page = 1 << c.page_log2;
 
-    // this block's share [t0, t1) of all tiles, and the batch row that t0 lies in
-    long long total = 0;
-    for (int b0 = 0; b0 < a.B; b0 += NT) {
-        long long sum;
-        block_scan(b0 + tid < a.B ? (long long)tiles_of(c, b0 + tid) * a.H : 0, &sum);
-        total += sum;
+    if (lane == 0) {
+        for (int i = 0; i < S; ++i) tc::mbar_init(&s_bar[warp][i], 1);
+        tc::mbar_fence_init();
+        s_piece[warp][0].u = s_piece[warp][1].u = -1;
     }
     if (blockIdx.x == 0 && tid == 0) *s.err = 0;
-    // no more blocks than tiles take part, so that no share is empty and the blocks that hold a
-    // unit follow one another
-    const long long nb = min((long long)gridDim.x, total);
-    if (blockIdx.x >= nb) return;
-    const long long t0 = total * blockIdx.x / nb, t1 = total * (blockIdx.x + 1) / nb;
+
+    // this warp's share [t0, t1) of all tiles, and the batch row that t0 lies in. No more warps
+    // than tiles take part, so no share is empty and the blocks of a unit follow one another.
+    long long total = 0, mine = 0, at = 0;
+    for (int b0 = 0; b0 < a.B; b0 += NT) {
+        long long sum;
+        mine = b0 + tid < a.B ? (long long)tiles_of<GR>(c, b0 + tid) * a.H : 0;
+        at = block_scan(mine, &sum);
+        total += sum;
+    }
+    const long long nw = min((long long)gridDim.x * WARPS, total);
+    const long long gw = (long long)blockIdx.x * WARPS + warp;
+    const long long t0 = gw < nw ? total * gw / nw : total, t1 = gw < nw ? total * (gw + 1) / nw : total;
+    Cursor cc{};
     long long cum = 0;
     for (int b0 = 0; b0 < a.B; b0 += NT) {
-        const long long mine = b0 + tid < a.B ? (long long)tiles_of(c, b0 + tid) * a.H : 0;
-        long long sum;
-        const long long at = cum + block_scan(mine, &sum);
-        if (at <= t0 && t0 < at + mine) {
-            s_row = b0 + tid;
-            s_cum = at;
+        long long sum = total;
+        if (a.B > NT) {
+            mine = b0 + tid < a.B ? (long long)tiles_of<GR>(c, b0 + tid) * a.H : 0;
+            at = block_scan(mine, &sum);
+        }
+        s_cum[tid] = cum + at;
+        __syncthreads();
+        if (t0 < t1 && cum <= t0 && t0 < cum + sum) {  // the last row whose tiles start at or before t0
+            int lo = 0, hi = min(NT, a.B - b0) - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) / 2;
+                if (s_cum[mid] <= t0)
+                    lo = mid;
+                else
+                    hi = mid - 1;
+            }
+            cc.at_row<GR>(c, b0 + lo);
+            const long long off = t0 - s_cum[lo];
+            cc.h = (int)(off / cc.nt);
+            cc.j = (int)(off % cc.nt);
         }
         cum += sum;
+        __syncthreads();
     }
-    __syncthreads();
-    int b = s_row;
-    cum = s_cum;
-    int nt = tiles_of(c, b);
-    const float scale2 = a.scale * LOG2E;
 
-    for (long long t = t0; t < t1;) {
-        while (t >= cum + (long long)nt * a.H) {  // next batch row with tiles
-            cum += (long long)nt * a.H;
-            nt = tiles_of(c, ++b);
-        }
-        const int slot = slot_of(c, b), n = length_of(c, slot);
-        const int h = (int)((t - cum) / nt), tb = (int)((t - cum) % nt);
-        const int te = (int)min((long long)nt, tb + (t1 - t));
-        const int u = b * a.H + h;
-        const int r1 = min(te * OWN_TILE, n + 1);
-        float w[V], q[V];
-        unpack<T>(reinterpret_cast<const uint4 *>(a.w)[(long long)u * LPR + lane_in_row], w);
-        unpack<T>(reinterpret_cast<const uint4 *>(a.q)[(long long)u * LPR + lane_in_row], q);
-        const float beta = a.beta[u];
-        const float lf = GATE ? a.log_f[u] : 0.f;
-        const int *tab = c.table + (long long)slot * c.max_pages;
-        uint4 *K = static_cast<uint4 *>(c.k), *Vp = static_cast<uint4 *>(c.v);
-        bool bad = false;
-        float m = -INFINITY, l = 0.f, acc[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) acc[i] = 0.f;
-        for (int rb = tb * OWN_TILE; rb < r1; rb += G * UNROLL) {
-            uint4 kv[UNROLL], vv[UNROLL];
-            long long at[UNROLL];  // row of the pool, or -1
-            float gv[UNROLL];
-#pragma unroll
-            for (int i = 0; i < UNROLL; ++i) {
-                const int r = rb + i * G + g;
-                at[i] = -1;
-                gv[i] = 0.f;
-                kv[i] = vv[i] = make_uint4(0u, 0u, 0u, 0u);
-                if (r < r1) {
-                    const int p = tab[r >> c.page_log2];
-                    if (p >= 0 && p < c.n_pages)
-                        at[i] = ((long long)p * a.H + h) * page + (r & (page - 1));
-                    else
-                        bad = true;
-                }
-                if (at[i] >= 0) {
-                    const bool fresh = r == n;
-                    kv[i] = fresh ? static_cast<const uint4 *>(a.k_new)[(long long)u * LPR + lane_in_row]
-                                  : K[at[i] * LPR + lane_in_row];
-                    vv[i] = fresh ? static_cast<const uint4 *>(a.v_new)[(long long)u * LPR + lane_in_row]
-                                  : Vp[at[i] * LPR + lane_in_row];
-                    if (GATE && !fresh) gv[i] = c.g[at[i]] + lf;
+    if (t0 < t1) {
+        const float scale2 = a.scale * LOG2E;
+        char *ring = smem + warp * C::RING;
+        float *gring = reinterpret_cast<float *>(smem + WARPS * C::RING) + warp * S * GR;
+        T *K = static_cast<T *>(c.k), *Vp = static_cast<T *>(c.v);
+
+        // the loads run ahead of the arithmetic by S granules
+        Cursor pc = cc;
+        int tab_b = -1, tab_at = 0, tab = -1;  // 32 entries of row tab_b's table, one a lane
+        long long tp = t0;
+        auto load = [&](int st) {
+            const int r0 = pc.j * GR, pg = r0 >> c.page_log2;
+            if (pc.b != tab_b || pg < tab_at || pg >= tab_at + 32) {
+                tab_b = pc.b;
+                tab_at = pg;
+                const int i = pg + lane;
+                tab = i < c.max_pages ? c.table[(long long)pc.slot * c.max_pages + i] : -1;
+            }
+            const int p = __shfl_sync(0xffffffffu, tab, pg - tab_at);
+            const bool ok = p >= 0 && p < c.n_pages;
+            const long long row = ((long long)p * a.H + pc.h) * page + (r0 & (page - 1));
+            if (lane == 0) {
+                s_row[warp][st] = ok ? row : -1;
+                uint64_t *bar = &s_bar[warp][st];
+                if (ok) {
+                    tc::mbar_expect_tx(bar, 2 * C::TILE + (GATE ? C::GATE : 0));
+                    tc::bulk_load(ring + st * 2 * C::TILE, K + row * D, C::TILE, bar);
+                    tc::bulk_load(ring + st * 2 * C::TILE + C::TILE, Vp + row * D, C::TILE, bar);
+                    if (GATE) tc::bulk_load(gring + st * GR, c.g + row, C::GATE, bar);
+                } else {
+                    tc::mbar_arrive(bar);
                 }
             }
+            ++tp;
+            advance<GR>(a, pc, t1 - tp);
+        };
+        for (int i = 0; i < S && tp < t1; ++i) load(i);
+
+        int st = 0, parity = 0, flags = 0, npiece = 0, u = -1, tb = 0;
+        bool dead = false;
+        float beta = 0.f, lf = 0.f, m = -INFINITY, l = 0.f;
+        F2 q[8], w[8], acc[8];
+        for (long long t = t0; t < t1; ++t) {
+            if (u != cc.b * a.H + cc.h) {  // a new unit
+                u = cc.b * a.H + cc.h;
+                tb = cc.j;
+                flags = 0;
+                beta = a.beta[u];
+                if (GATE) lf = a.log_f[u];
 #pragma unroll
-            for (int i = 0; i < UNROLL; ++i) {
-                const int r = rb + i * G + g;
-                const bool valid = at[i] >= 0, fresh = r == n;
-                float k[V], v[V];
-                unpack<T>(kv[i], k);
-                unpack<T>(vv[i], v);
-                float wk = 0.f;
-#pragma unroll
-                for (int e = 0; e < V; ++e) wk = fmaf(w[e], k[e], wk);
-                const float coef = beta * group_sum<LPR>(wk);
-                if (!fresh) {
-#pragma unroll
-                    for (int e = 0; e < V; ++e) k[e] = fmaf(-coef, w[e], k[e]);
+                for (int j = 0; j < CPL; ++j) {
+                    const long long x = (long long)u * C::ROW_CHUNKS + lr + LPR * (j ^ odd);
+                    to_pairs<T>(static_cast<const uint4 *>(a.q)[x], q + j * VP);
+                    to_pairs<T>(static_cast<const uint4 *>(a.w)[x], w + j * VP);
                 }
-                if (valid) {
-                    K[at[i] * LPR + lane_in_row] = fresh ? kv[i] : pack<T>(k);
-                    if (fresh) Vp[at[i] * LPR + lane_in_row] = vv[i];
-                    if (GATE && lane_in_row == 0) c.g[at[i]] = gv[i];
+                m = -INFINITY;
+                l = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) acc[i] = 0ull;
+            }
+            if (!tc::mbar_wait(&s_bar[warp][st], parity, dead ? 0 : tc::WAIT_LIMIT_NS)) dead = true;
+            dead = __any_sync(0xffffffffu, dead);
+            const long long row0 = s_row[warp][st];
+            const int r0 = cc.j * GR, n = cc.n;
+            if (dead) flags |= GAVE_UP;
+            if (row0 < 0) flags |= BAD_PAGE;
+            const uint4 *tk = reinterpret_cast<const uint4 *>(ring + st * 2 * C::TILE);
+            const uint4 *tv = tk + C::TILE / 16;
+            auto granule = [&](auto tail_tag) {
+                constexpr bool TAIL = decltype(tail_tag)::value;
+                float z[C::PASSES];
+#pragma unroll
+                for (int i = 0; i < C::PASSES; ++i) {
+                    const int ri = i * RPP + grp, r = r0 + ri;
+                    const bool valid = !TAIL || r <= n, fresh = TAIL && r == n;
+                    uint4 kc[CPL];
+                    F2 k[8];
+#pragma unroll
+                    for (int j = 0; j < CPL; ++j) {
+                        const int x = lr + LPR * (j ^ odd);
+                        kc[j] = fresh ? static_cast<const uint4 *>(a.k_new)[(long long)u * C::ROW_CHUNKS + x]
+                                      : tk[ri * C::ROW_CHUNKS + x];
+                        to_pairs<T>(kc[j], k + j * VP);
+                    }
+                    const float nc = -(beta * group_sum<LPR>(dot16(w, k)));
+                    const F2 nc2 = f2(nc, nc);
+                    if (!TAIL || !fresh) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) k[e] = fma2(nc2, w[e], k[e]);
+                    }
+                    uint4 *dst = reinterpret_cast<uint4 *>(K + (row0 + ri) * D);
+#pragma unroll
+                    for (int j = 0; j < CPL; ++j) {
+                        const int x = lr + LPR * (j ^ odd);
+                        if (!TAIL || !fresh) kc[j] = from_pairs<T>(k + j * VP);
+                        if (valid) dst[x] = kc[j];
+                        if (sizeof(T) == 2) to_pairs<T>(kc[j], k + j * VP);  // the key as it is stored
+                    }
+                    float bias = 0.f;
+                    if (GATE) {
+                        bias = fresh ? 0.f : gring[st * GR + ri] + lf;
+                        if (valid && lr == 0) c.g[row0 + ri] = bias;
+                    }
+                    z[i] = fmaf(group_sum<LPR>(dot16(q, k)), scale2, bias * LOG2E);
+                    if (!valid) z[i] = -INFINITY;
                 }
-                if (!fresh) round_to<T>(k);
-                float z = 0.f;
+                float mn = m;
 #pragma unroll
-                for (int e = 0; e < V; ++e) z = fmaf(q[e], k[e], z);
-                z = fmaf(group_sum<LPR>(z), scale2, gv[i] * LOG2E);
-                if (valid) {
-                    const float mn = fmaxf(m, z);
-                    if (mn != -INFINITY) {  // all -inf so far: nothing to weigh
-                        const float corr = tc::ex2(m - mn), p = tc::ex2(z - mn);
-                        l = fmaf(l, corr, p);
+                for (int i = 0; i < C::PASSES; ++i) mn = fmaxf(mn, z[i]);
+                const float base = mn == -INFINITY ? 0.f : mn;  // nothing weighs yet
+                const float corr = tc::ex2(m - base);
+                m = mn;
+                l *= corr;
+                const F2 c2 = f2(corr, corr);
 #pragma unroll
-                        for (int e = 0; e < V; ++e) acc[e] = fmaf(acc[e], corr, p * v[e]);
-                        m = mn;
-                    } else if (isnan(z)) {
-                        l = z;
+                for (int e = 0; e < 8; ++e) acc[e] = mul2(acc[e], c2);
+#pragma unroll
+                for (int i = 0; i < C::PASSES; ++i) {
+                    const int ri = i * RPP + grp, r = r0 + ri;
+                    const bool valid = !TAIL || r <= n, fresh = TAIL && r == n;
+                    const float p = tc::ex2(z[i] - base);
+                    l += p;
+                    const F2 p2 = f2(p, p);
+#pragma unroll
+                    for (int j = 0; j < CPL; ++j) {
+                        const int x = lr + LPR * (j ^ odd);
+                        uint4 vc = make_uint4(0u, 0u, 0u, 0u);  // a row behind the last counts nothing
+                        if (fresh) {
+                            vc = static_cast<const uint4 *>(a.v_new)[(long long)u * C::ROW_CHUNKS + x];
+                            reinterpret_cast<uint4 *>(Vp + (row0 + ri) * D)[x] = vc;
+                        } else if (valid) {
+                            vc = tv[ri * C::ROW_CHUNKS + x];
+                        }
+                        F2 v[VP];
+                        to_pairs<T>(vc, v);
+#pragma unroll
+                        for (int e = 0; e < VP; ++e) acc[j * VP + e] = fma2(p2, v[e], acc[j * VP + e]);
+                    }
+                }
+            };
+            if (row0 >= 0 && !dead) {
+                if (r0 + GR > n)
+                    granule(std::true_type{});
+                else
+                    granule(std::false_type{});
+            }
+            __syncwarp();  // the stage has been read
+            if (tp < t1 && !dead) load(st);
+            if (++st == S) {
+                st = 0;
+                parity ^= 1;
+            }
+            const bool ends = cc.j + 1 == cc.nt;
+            const int u_done = u;
+            const bool whole = ends && tb == 0;
+            if (ends || t + 1 == t1) {  // the row groups join; then lanes 0 .. LPR - 1 hold the row
+                float M = m;
+#pragma unroll
+                for (int o = LPR; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+                const float f = m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : tc::ex2(m - M);
+                float L = l * f, x[16];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) split(acc[e], x[2 * e], x[2 * e + 1]);
+                if (LPR == 4) {  // odd rows hold neighbouring chunks in the other order
+                    constexpr int N = Vec<T>::N;
+#pragma unroll
+                    for (int j = 0; j < CPL; j += 2)
+#pragma unroll
+                        for (int e = 0; e < N; ++e) {
+                            const float y0 = x[j * N + e], y1 = x[(j + 1) * N + e];
+                            x[j * N + e] = odd ? y1 : y0;
+                            x[(j + 1) * N + e] = odd ? y0 : y1;
+                        }
+                }
+#pragma unroll
+                for (int e = 0; e < 16; ++e) x[e] *= f;
+#pragma unroll
+                for (int o = LPR; o < 32; o <<= 1) {
+                    L += __shfl_xor_sync(0xffffffffu, L, o);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) x[e] += __shfl_xor_sync(0xffffffffu, x[e], o);
+                }
+                flags |= (tb == 0 ? FIRST : 0) | (ends ? LAST : 0);
+                if (whole) {
+                    const float nan = __int_as_float(0x7fc00000);
+                    const long long piece = (long long)blockIdx.x + u_done;
+                    const bool bad = flags & (BAD_PAGE | GAVE_UP);
+                    if (lane < LPR) {
+                        const float inv = bad ? nan : 1.f / L;
+                        float *part = s.own + piece * (D + 2);
+#pragma unroll
+                        for (int j = 0; j < CPL; ++j) {
+                            constexpr int N = Vec<T>::N;
+                            const int ch = lane + LPR * j;
+                            if (SHARED) {
+#pragma unroll
+                                for (int e = 0; e < N; e += 2)
+                                    *reinterpret_cast<float2 *>(part + 2 + ch * N + e) =
+                                        make_float2(x[j * N + e], x[j * N + e + 1]);
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < N; ++e) x[j * N + e] *= inv;
+                                T *o = static_cast<T *>(a.out) + (long long)u_done * D + ch * N;
+#pragma unroll
+                                for (int e = 0; e < N; ++e) o[e] = from_f<T>(x[j * N + e]);
+                            }
+                        }
+                        if (SHARED && lane == 0) {
+                            part[0] = M;
+                            part[1] = L;
+                        }
+                    }
+                    if (lane == 0) {
+                        s.own_flag[piece] = flags;
+                        s.first[u_done] = s.last[u_done] = blockIdx.x;
+                    }
+                } else {
+                    Piece<D> &pp = s_piece[warp][npiece++];
+                    if (lane < LPR) {
+#pragma unroll
+                        for (int j = 0; j < CPL; ++j) {
+                            constexpr int N = Vec<T>::N;
+#pragma unroll
+                            for (int e = 0; e < N; ++e) pp.acc[(lane + LPR * j) * N + e] = x[j * N + e];
+                        }
+                    }
+                    if (lane == 0) {
+                        pp.u = u_done;
+                        pp.flags = flags;
+                        pp.m = M;
+                        pp.l = L;
                     }
                 }
             }
+            advance<GR>(a, cc, t1 - t - 1);
         }
-        // join the row groups of this block
-        if (lane_in_row == 0) {
-            s_m[g] = m;
-            s_l[g] = l;
+        if (dead)  // copies may still be on their way into this block's memory
+            for (int i = 0; i < S; ++i)
+                tc::mbar_wait(&s_bar[warp][(st + i) % S], st + i < S ? parity : parity ^ 1, tc::WAIT_LIMIT_NS);
+    }
+    __syncthreads();
+
+    // The pieces of the block's warps, in order: neighbours of one unit are put together.
+    const Piece<D> *pieces = &s_piece[0][0];
+    for (int i = 0; i < 2 * WARPS;) {
+        const int u = pieces[i].u;
+        if (u < 0) {
+            ++i;
+            continue;
         }
-#pragma unroll
-        for (int i = 0; i < V; ++i) s_acc[g][lane_in_row * V + i] = acc[i];
-        const bool any_bad = __syncthreads_or(bad);
-        const bool whole = tb == 0 && te == nt;
+        int end = i, flags = 0;
+        float M = -INFINITY;
+        for (; end < 2 * WARPS && (pieces[end].u == u || pieces[end].u < 0); ++end) {
+            if (pieces[end].u < 0) continue;
+            flags |= pieces[end].flags;
+            M = fmaxf(M, pieces[end].m);
+        }
         const long long piece = (long long)blockIdx.x + u;
         if (tid < D) {
-            float M = -INFINITY;
-            for (int j = 0; j < G; ++j) M = fmaxf(M, s_m[j]);
             float L = 0.f, A = 0.f;
-            for (int j = 0; j < G; ++j) {
-                const float f = s_m[j] == -INFINITY ? (s_l[j] == 0.f ? 0.f : 1.f) : tc::ex2(s_m[j] - M);
-                L = fmaf(s_l[j], f, L);
-                A = fmaf(s_acc[j][tid], f, A);
+            for (int k = i; k < end; ++k) {
+                if (pieces[k].u < 0) continue;
+                const float mk = pieces[k].m, lk = pieces[k].l;
+                const float f = mk == -INFINITY ? (lk == 0.f ? 0.f : 1.f) : tc::ex2(mk - M);
+                L = fmaf(lk, f, L);
+                A = fmaf(pieces[k].acc[tid], f, A);
             }
-            if (any_bad) M = L = A = __int_as_float(0x7fc00000);
-            if (whole && !SHARED) {
+            if (flags & (BAD_PAGE | GAVE_UP)) L = A = __int_as_float(0x7fc00000);
+            if ((flags & FIRST) && (flags & LAST) && !SHARED) {
                 static_cast<T *>(a.out)[(long long)u * D + tid] = from_f<T>(A / L);
             } else {
                 float *part = s.own + piece * (D + 2);
@@ -217,12 +513,11 @@ __global__ void __launch_bounds__(NT) decode_own_kernel(PagedStep a, PagedScratc
             }
         }
         if (tid == 0) {
-            s.own_flag[piece] = any_bad;
-            if (tb == 0) s.first[u] = blockIdx.x;
-            if (te == nt) s.last[u] = blockIdx.x;
+            s.own_flag[piece] = flags;
+            if (flags & FIRST) s.first[u] = blockIdx.x;
+            if (flags & LAST) s.last[u] = blockIdx.x;
         }
-        __syncthreads();
-        t += te - tb;
+        i = end;
     }
 }
 
@@ -257,9 +552,10 @@ __global__ void __launch_bounds__(D) decode_join_kernel(PagedStep a, PagedScratc
         const long long total = (long long)p.pre_units * p.key_tiles, t0 = pu * p.key_tiles;
         j0 = (int)(((t0 + 1) * p.pre_blocks - 1) / total);
         j1 = (int)(((t0 + p.key_tiles) * p.pre_blocks - 1) / total);
-        for (int j = j0; j <= j1; ++j) flag |= s.pre_flag[j + pu];
+        for (int j = j0; j <= j1; ++j) flag |= s.pre_flag[j + pu] ? BAD_PAGE : 0;
     }
-    if (flag && e == 0) atomicMax(s.err, ERR_PAGE);
+    flag &= BAD_PAGE | GAVE_UP;
+    if (flag && e == 0) atomicMax(s.err, flag & BAD_PAGE ? ERR_PAGE : ERR_OWN_WAIT);
     if (!SHARED && i0 == i1) return;  // one block held the whole unit and wrote out
     float M = -INFINITY;
     for (int i = i0; i <= i1; ++i) M = fmaxf(M, s.own[((long long)i + u) * (D + 2)]);
@@ -286,12 +582,13 @@ cudaError_t run(const PagedStep &a, const PagedPlan &p, const PagedScratch &s, c
 {
     {
         Stage stage("decode_own", st);
-        if (a.c.g)
-            decode_own_kernel<T, D, true, SHARED><<<p.own_blocks, NT, 0, st>>>(a, s);
-        else
-            decode_own_kernel<T, D, false, SHARED><<<p.own_blocks, NT, 0, st>>>(a, s);
+        auto k = a.c.g ? decode_own_kernel<T, D, true, SHARED> : decode_own_kernel<T, D, false, SHARED>;
+        constexpr int smem = OwnCfg<T, D>::SMEM;
+        cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        k<<<p.own_blocks, NT, smem, st>>>(a, s);
         count_launches();
-        cudaError_t e = cudaGetLastError();
+        e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
     Stage stage("decode_join", st);
@@ -312,11 +609,10 @@ PagedPlan paged_plan(int B, int H, int max_pages, int page, int d, int dt, int p
 {
     PagedPlan p;
     const int sms = sm_count();
-    const long long most = (long long)B * H * (((long long)max_pages * page - 1) / OWN_TILE + 1);
-    long long blocks = 2LL * sms;
-    if (blocks > OWN_MAX_BLOCKS) blocks = OWN_MAX_BLOCKS;
-    if (blocks > most) blocks = most;
-    p.own_blocks = (int)blocks;
+    const int gr = own_granule(d, (int)dtype_size(dt));
+    const long long most = (long long)B * H * (((long long)max_pages * page - 1) / gr + 1);
+    const long long blocks = (most + WARPS - 1) / WARPS;
+    p.own_blocks = (int)(blocks < sms ? blocks : sms);
     p.own_slots = p.own_blocks + B * H;
     p.q_tile = 32;
     p.key_tile = 64;

@@ -46,13 +46,11 @@ __device__ __forceinline__ int length_of(const PagedCache &c, int slot)
     return n >= 0 && n < (long long)c.max_pages << c.page_log2 ? n : -1;
 }
 
-// Key tile of the own part: work is dealt out in tiles of this many rows.
-constexpr int OWN_TILE = 64;
-// Upper bound on the blocks of the own part (its partials' slots).
-constexpr int OWN_MAX_BLOCKS = 1024;
+// Rows of a tile of the own part: 8 KB of keys and values, or 16 rows (the smallest page).
+constexpr int own_granule(int d, int size) { return d * size == 512 ? 8 : 16; }
 
 // Device error codes of a paged step (first word of the workspace)
-constexpr int ERR_PAGE = 1000;
+constexpr int ERR_PAGE = 1000, ERR_OWN_WAIT = 41;
 
 // Scratch of a step, carved from the caller's workspace.
 //

@@ -389,7 +389,9 @@ def test_repeats_exactly_on_another_stream_and_in_graphs(P, prefix):
 
 
 def test_paged_agrees_with_contiguous_decode(P):
-    """Equal lengths: the same keys, bit for bit, as path_decode_step leaves, and its outputs."""
+    """Equal lengths: path_decode_step's keys and outputs. Both steps add up w.k in an order of
+    their own and round once, so a key may land on the neighbouring bf16 number (one step,
+    2^-7 relative, plus the fp32 error of two updates); values and the new row are copies."""
     B, H, d, page, n = 3, 4, 128, 32, 333
     g = torch.Generator(device="cuda").manual_seed(1)
     kc = torch.randn((B, H, n + 1, d), device="cuda", generator=g).to(BF)
@@ -404,7 +406,9 @@ def test_paged_agrees_with_contiguous_decode(P):
     out = P.path_decode_step_paged(x["q"], x["k_new"], x["v_new"], x["w"], x["beta"], k, v, table, ints([n] * B))
     rows = lambda t, b: torch.cat([t[p] for p in table[b].tolist()], 1)[:, : n + 1]
     for b in range(B):
-        assert torch.equal(rows(k, b), kc[b]) and torch.equal(rows(v, b), vc[b])
+        a, b_ = rows(k, b).float(), kc[b].float()
+        assert ((a - b_).abs() <= 2.0 ** -7 * b_.abs() + 2 * 2.0 ** -24 * 8 * math.sqrt(d) * 2 * b_.norm(dim=-1, keepdim=True)).all()
+        assert torch.equal(rows(k, b)[:, n], kc[b][:, n]) and torch.equal(rows(v, b), vc[b])
     assert (out.float() - want.float()).abs().max() <= 2 * 2.0 ** -8 * want.float().abs().max()
 
 

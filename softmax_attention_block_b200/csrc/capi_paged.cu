@@ -58,8 +58,8 @@ path_status step_args(const void *q, const void *k_new, const void *v_new, const
     if (s != PATH_OK) return s;
     if ((d != 64 && d != 128) || !kv_dtype_ok(dt) || (long long)B * H > 65535 || !pool_fits(n_pages, H, page))
         return PATH_ERR_UNSUPPORTED;
-    // 16-byte vector access
-    for (const void *p : {q, k_new, v_new, w, (const void *)k_pages, (const void *)v_pages})
+    // 16-byte vector access and bulk copies
+    for (const void *p : {q, k_new, v_new, w, (const void *)k_pages, (const void *)v_pages, (const void *)g_pages})
         if (!aligned(p, 16)) return PATH_ERR_INVALID_ARG;
     a = PagedStep{};
     a.q = q;
@@ -137,7 +137,7 @@ path_status path_decode_step_shared(const void *q, const void *k_new, const void
     paged_carve(workspace, p, B, H, d, s);
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     TRY(prefix_turn(a, (int)dt, d, p, s, cs));
-    TRY(prefix_attn_simt(a, (int)dt, d, p, s, cs));
+    TRY(dt == PATH_BF16 ? prefix_attn_tc(a, d, p, s, cs) : prefix_attn_simt(a, d, p, s, cs));
     return launch_status(decode_paged(a, (int)dt, d, true, p, s, cs));
 }
 

@@ -167,7 +167,7 @@ struct Piece {
     float m, l;
     float acc[D];
 };
-enum { FIRST = 1, LAST = 2, BAD_PAGE = 4, GAVE_UP = 8 };
+enum { FIRST = 1, LAST = 2, BAD_PAGE = PIECE_BAD_PAGE, GAVE_UP = PIECE_GAVE_UP };
 
 template <typename T, int D, bool GATE, bool SHARED>
 __global__ void __launch_bounds__(NT, 1) decode_own_kernel(PagedStep a, PagedScratch s)
@@ -552,10 +552,10 @@ __global__ void __launch_bounds__(D) decode_join_kernel(PagedStep a, PagedScratc
         const long long total = (long long)p.pre_units * p.key_tiles, t0 = pu * p.key_tiles;
         j0 = (int)(((t0 + 1) * p.pre_blocks - 1) / total);
         j1 = (int)(((t0 + p.key_tiles) * p.pre_blocks - 1) / total);
-        for (int j = j0; j <= j1; ++j) flag |= s.pre_flag[j + pu] ? BAD_PAGE : 0;
+        for (int j = j0; j <= j1; ++j) flag |= s.pre_flag[j + pu];
     }
     flag &= BAD_PAGE | GAVE_UP;
-    if (flag && e == 0) atomicMax(s.err, flag & BAD_PAGE ? ERR_PAGE : ERR_OWN_WAIT);
+    if (flag && e == 0) atomicMax(s.err, flag & BAD_PAGE ? ERR_PAGE : ERR_PAGED_WAIT);
     if (!SHARED && i0 == i1) return;  // one block held the whole unit and wrote out
     float M = -INFINITY;
     for (int i = i0; i <= i1; ++i) M = fmaxf(M, s.own[((long long)i + u) * (D + 2)]);
@@ -614,13 +614,15 @@ PagedPlan paged_plan(int B, int H, int max_pages, int page, int d, int dt, int p
     const long long blocks = (most + WARPS - 1) / WARPS;
     p.own_blocks = (int)(blocks < sms ? blocks : sms);
     p.own_slots = p.own_blocks + B * H;
-    p.q_tile = 32;
-    p.key_tile = 64;
+    // bf16: the prefix is read once for 64 queries, or for 32 with half the softmax; fp32: CUDA cores
+    p.q_tile = dt == BF16 && B > 32 ? 64 : 32;
+    p.key_tile = dt == BF16 ? 128 : 64;
     p.q_tiles = ceil_div(B, p.q_tile);
     p.key_tiles = (int)(((long long)prefix_len + p.key_tile - 1) / p.key_tile);
     p.pre_units = p.q_tiles * H;
     const long long tiles = (long long)p.pre_units * p.key_tiles;
-    p.pre_blocks = (int)(tiles < 2LL * sms ? tiles : 2LL * sms);
+    const int most_blocks = dt == BF16 ? sms : 2 * sms;
+    p.pre_blocks = (int)(tiles < most_blocks ? tiles : most_blocks);
     p.pre_slots = prefix_len > 0 ? p.pre_blocks + p.pre_units : 0;
     return p;
 }

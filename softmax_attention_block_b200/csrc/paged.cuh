@@ -49,8 +49,11 @@ __device__ __forceinline__ int length_of(const PagedCache &c, int slot)
 // Rows of a tile of the own part: 8 KB of keys and values, or 16 rows (the smallest page).
 constexpr int own_granule(int d, int size) { return d * size == 512 ? 8 : 16; }
 
+// What went wrong with a piece (bits of own_flag and pre_flag)
+enum { PIECE_BAD_PAGE = 4, PIECE_GAVE_UP = 8 };
+
 // Device error codes of a paged step (first word of the workspace)
-constexpr int ERR_PAGE = 1000, ERR_OWN_WAIT = 41;
+constexpr int ERR_PAGE = 1000, ERR_PAGED_WAIT = 41;
 
 // Scratch of a step, carved from the caller's workspace.
 //
@@ -63,8 +66,10 @@ struct PagedScratch {
     int *err;          // [64]
     int *first, *last; // [B * H] blocks of a unit's first and last tile
     float *own;        // [own_slots, d + 2]: max (log2 domain), sum, accumulator
-    int *own_flag;     // [own_slots] nonzero: a page was out of range
-    float *qt;         // [H, q_rows, d] the queries turned back to the prefix's end
+    int *own_flag;     // [own_slots] bits 2, 3: see PIECE_*
+    // the queries turned back to the prefix's end, q_rows = q_tiles * q_tile of a head (zero past
+    // the batch): [H, q_rows, d] fp32, or for the tensor cores [2, H, q_rows, d] bf16, hi and lo
+    float *qt;
     float *qg;         // [H, q_rows] the gate's bias since the prefix's end (log2 domain)
     float *pre;        // [pre_slots, q_tile, d] accumulators of the prefix part
     float *pre_ml;     // [pre_slots, 2, q_tile] max (log2 domain) and sum
@@ -82,7 +87,10 @@ size_t paged_carve(void *base, const PagedPlan &p, int B, int H, int d, PagedScr
 // state <- H state, and the queries the prefix sees (SHARED only)
 cudaError_t prefix_turn(const PagedStep &a, int dt, int d, const PagedPlan &p, const PagedScratch &s,
                         cudaStream_t st);
-cudaError_t prefix_attn_simt(const PagedStep &a, int dt, int d, const PagedPlan &p,
+// The batch's attention to the prefix: fp32 on CUDA cores, bf16 on the tensor cores.
+cudaError_t prefix_attn_tc(const PagedStep &a, int d, const PagedPlan &p, const PagedScratch &s,
+                           cudaStream_t st);
+cudaError_t prefix_attn_simt(const PagedStep &a, int d, const PagedPlan &p,
                              const PagedScratch &s, cudaStream_t st);
 // The sequences' own pages (in-place key update, softmax pieces), then the
 // join of all pieces of a row, the prefix's included.

@@ -32,11 +32,19 @@ __global__ void __launch_bounds__(NT) turn_kernel(PagedStep a, PagedScratch s, i
     __shared__ float4 red[2][RG][CG];
     const int u = blockIdx.x, b = u / a.H, h = u % a.H, tid = threadIdx.x;
     const int cg = tid % CG, rg = tid / CG;
-    const int slot = slot_of(a.c, b);
-    float *qt = s.qt + ((long long)h * q_rows + b) * D;
-    if (slot < 0 || length_of(a.c, slot) < 0) {  // idle or invalid: a query of zeros, not read
-        if (tid < D) qt[tid] = 0.f;
-        if (tid == 0) s.qg[(long long)h * q_rows + b] = 0.f;
+    const int slot = b < a.B ? slot_of(a.c, b) : -1;
+    const long long row = (long long)h * q_rows + b;
+    float4 *qt = reinterpret_cast<float4 *>(s.qt) + row * CG;  // fp32
+    uint2 *qhi = reinterpret_cast<uint2 *>(s.qt) + row * CG;   // bf16, hi and lo
+    uint2 *qlo = qhi + (long long)a.H * q_rows * CG;
+    if (slot < 0 || length_of(a.c, slot) < 0) {  // past the batch, idle or invalid: a query of zeros
+        if (tid < CG) {
+            if (sizeof(T) == 4)
+                qt[tid] = make_float4(0.f, 0.f, 0.f, 0.f);
+            else
+                qhi[tid] = qlo[tid] = make_uint2(0u, 0u);
+        }
+        if (tid == 0) s.qg[row] = 0.f;
         return;
     }
     if (tid < D) {
@@ -96,8 +104,21 @@ __global__ void __launch_bounds__(NT) turn_kernel(PagedStep a, PagedScratch s, i
             z.w += t.w;
         }
         const float f = -beta * qw;
-        reinterpret_cast<float4 *>(qt)[cg] =
-            make_float4(fmaf(f, y.x, z.x), fmaf(f, y.y, z.y), fmaf(f, y.z, z.z), fmaf(f, y.w, z.w));
+        const float4 r = make_float4(fmaf(f, y.x, z.x), fmaf(f, y.y, z.y), fmaf(f, y.z, z.z), fmaf(f, y.w, z.w));
+        if (sizeof(T) == 4) {
+            qt[cg] = r;
+        } else {  // r = hi + lo to 2^-17
+            const float v[4] = {r.x, r.y, r.z, r.w};
+            __nv_bfloat162 hi[2], lo[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                hi[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+                const float2 t = __bfloat1622float2(hi[i]);
+                lo[i] = __floats2bfloat162_rn(v[2 * i] - t.x, v[2 * i + 1] - t.y);
+            }
+            qhi[cg] = *reinterpret_cast<uint2 *>(hi);
+            qlo[cg] = *reinterpret_cast<uint2 *>(lo);
+        }
     }
     if (tid == 0) {
         float g = 0.f;
@@ -106,7 +127,7 @@ __global__ void __launch_bounds__(NT) turn_kernel(PagedStep a, PagedScratch s, i
             g = *gs + a.log_f[u];
             *gs = g;
         }
-        s.qg[(long long)h * q_rows + b] = g * LOG2E;
+        s.qg[row] = g * LOG2E;
     }
 }
 
@@ -122,33 +143,29 @@ struct SimtCfg {
     static constexpr int SMEM = (G + KT) * 4;
 };
 
-// Rows of a key tile into shared memory as fp32; rows past the prefix are zero.
-template <typename T, int D>
+// Rows of a key tile into shared memory; rows past the prefix are zero.
+template <int D>
 __device__ __forceinline__ bool load_tile(const void *pool, const PagedStep &a, int h, int key0, float *dst, int ld)
 {
-    constexpr int V = Vec<T>::N, LPR = D / V;
+    constexpr int LPR = D / 4;
     bool bad = false;
     for (int i = threadIdx.x; i < KT * LPR; i += NT) {
         const int r = i / LPR, x = i % LPR, key = key0 + r;
-        uint4 u = make_uint4(0u, 0u, 0u, 0u);
+        float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
         if (key < a.prefix_len) {
             const int p = a.prefix_table[key >> a.c.page_log2];
             if (p >= 0 && p < a.c.n_pages)
-                u = static_cast<const uint4 *>(pool)[((((long long)p * a.H + h) << a.c.page_log2) +
-                                                      (key & ((1 << a.c.page_log2) - 1))) * LPR + x];
+                f = static_cast<const float4 *>(pool)[((((long long)p * a.H + h) << a.c.page_log2) +
+                                                       (key & ((1 << a.c.page_log2) - 1))) * LPR + x];
             else
                 bad = true;
         }
-        float f[V];
-        unpack<T>(u, f);
-#pragma unroll
-        for (int e = 0; e < V; e += 4)
-            *reinterpret_cast<float4 *>(dst + r * ld + x * V + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+        *reinterpret_cast<float4 *>(dst + r * ld + 4 * x) = f;
     }
     return bad;
 }
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(NT) prefix_simt_kernel(PagedStep a, PagedScratch s, PagedPlan p)
 {
     using C = SimtCfg<D>;
@@ -178,8 +195,8 @@ __global__ void __launch_bounds__(NT) prefix_simt_kernel(PagedStep a, PagedScrat
         for (int kt = kb; kt < ke; ++kt) {
             const int key0 = kt * KT;
             __syncthreads();  // the former tile is done with
-            bad |= load_tile<T, D>(a.c.k, a, h, key0, sK, LD);
-            bad |= load_tile<T, D>(a.c.v, a, h, key0, sV, D);
+            bad |= load_tile<D>(a.c.k, a, h, key0, sK, LD);
+            bad |= load_tile<D>(a.c.v, a, h, key0, sV, D);
             if (tid < KT) {
                 const int key = key0 + tid;
                 float g = -INFINITY;  // a key past the prefix
@@ -272,15 +289,15 @@ __global__ void __launch_bounds__(NT) prefix_simt_kernel(PagedStep a, PagedScrat
                 }
             }
         }
-        if (tid == 0) s.pre_flag[piece] = any_bad;
+        if (tid == 0) s.pre_flag[piece] = any_bad ? PIECE_BAD_PAGE : 0;
         t += ke - kb;
     }
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t run_simt(const PagedStep &a, const PagedPlan &p, const PagedScratch &s, cudaStream_t st)
 {
-    auto k = prefix_simt_kernel<T, D>;
+    auto k = prefix_simt_kernel<D>;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SimtCfg<D>::SMEM);
     if (e != cudaSuccess) return e;
     k<<<p.pre_blocks, NT, SimtCfg<D>::SMEM, st>>>(a, s, p);
@@ -291,7 +308,8 @@ cudaError_t run_simt(const PagedStep &a, const PagedPlan &p, const PagedScratch 
 template <typename T, int D>
 cudaError_t run_turn(const PagedStep &a, const PagedPlan &p, const PagedScratch &s, cudaStream_t st)
 {
-    turn_kernel<T, D><<<a.B * a.H, NT, 0, st>>>(a, s, p.q_tiles * p.q_tile);
+    const int q_rows = p.q_tiles * p.q_tile;
+    turn_kernel<T, D><<<q_rows * a.H, NT, 0, st>>>(a, s, q_rows);
     count_launches();
     return cudaGetLastError();
 }
@@ -307,13 +325,11 @@ cudaError_t prefix_turn(const PagedStep &a, int dt, int d, const PagedPlan &p, c
     return cudaErrorInvalidValue;
 }
 
-cudaError_t prefix_attn_simt(const PagedStep &a, int dt, int d, const PagedPlan &p,
+cudaError_t prefix_attn_simt(const PagedStep &a, int d, const PagedPlan &p,
                              const PagedScratch &s, cudaStream_t st)
 {
     Stage stage("prefix_attn", st);
-    if (d == 64) return dt == F32 ? run_simt<float, 64>(a, p, s, st) : run_simt<bf16, 64>(a, p, s, st);
-    if (d == 128) return dt == F32 ? run_simt<float, 128>(a, p, s, st) : run_simt<bf16, 128>(a, p, s, st);
-    return cudaErrorInvalidValue;
+    return d == 64 ? run_simt<64>(a, p, s, st) : run_simt<128>(a, p, s, st);
 }
 
 }  // namespace path

@@ -59,6 +59,9 @@ def test_step_refusals(lib, shared):
         assert step(lib, shared, **{n: FAKE + 8}) == INVALID, n
     for n in ("B", "H", "N", "R", "M"):
         assert step(lib, shared, **{n: 0}) == INVALID, n
+    gate = dict(log_f=FAKE, gs=FAKE)
+    assert step(lib, shared, g=FAKE, **gate) == WORKSPACE
+    assert step(lib, shared, g=FAKE + 8, **gate) == INVALID
     assert step(lib, shared, scale=float("inf")) == INVALID
     assert step(lib, shared, log_f=FAKE) == INVALID
     assert step(lib, shared, g=FAKE) == INVALID

@@ -36,20 +36,26 @@ struct OwnCfg {
     static constexpr int TILE = GR * D * (int)sizeof(T);
     static constexpr int STAGES = 24576 / (2 * TILE);
     static constexpr int GATE = GR * 4;
-    // shared memory: the warps' rings, then the gate biases
-    static constexpr int RING = STAGES * 2 * TILE;
-    static constexpr int SMEM = WARPS * (RING + STAGES * GATE);
+    static constexpr int ROW = D * (int)sizeof(T);
+    // shared memory of a warp: a ring of key and value tiles, its units' q and w, its gate biases
+    static constexpr int RING = STAGES * 2 * TILE, HEAD = STAGES * 2 * ROW;
+    static constexpr int SMEM = WARPS * (RING + HEAD + STAGES * GATE);
     static_assert(GR % RPP == 0 && STAGES >= 2 && TILE % 128 == 0, "granule");
 };
 
-// Tiles (granules) of one head of batch row b (0: idle or invalid; the new token is a row).
+// Starting and ending a unit (one head of one batch row) takes a warp about as long as one
+// granule, and the shares are dealt out with it: 96 rows of 0 to 512 tokens, 24 heads of 64, take
+// 50 us instead of 67 without it and 51 with 2; long rows do not notice.
+constexpr int UNIT_COST = 1;
+
+// Cost of one head of batch row b (0: idle or invalid; the new token is a row).
 template <int GR>
-__device__ __forceinline__ int tiles_of(const PagedCache &c, int b)
+__device__ __forceinline__ int cost_of(const PagedCache &c, int b)
 {
     const int slot = slot_of(c, b);
     if (slot < 0) return 0;
     const int n = length_of(c, slot);
-    return n < 0 ? 0 : n / GR + 1;
+    return n < 0 ? 0 : n / GR + 1 + UNIT_COST;
 }
 
 __device__ long long block_scan(long long x, long long *total)
@@ -73,31 +79,6 @@ __device__ long long block_scan(long long x, long long *total)
     __syncthreads();
     *total = sum;
     return before + v - x;
-}
-
-// Pairs of fp32 numbers in one 64-bit register: one instruction for two products.
-typedef unsigned long long F2;
-__device__ __forceinline__ F2 f2(float lo, float hi)
-{
-    F2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ void split(F2 x, float &lo, float &hi)
-{
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
-{
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b)
-{
-    F2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
 }
 
 // One 16-byte chunk to pairs, N of them.
@@ -133,10 +114,12 @@ __device__ __forceinline__ float dot16(const F2 *a, const F2 *b)
     return (x0 + y0) + (x1 + y1);
 }
 
-// Position in the list of all tiles: unit (b, h), tile j of its nt.
+// Position in the list of all granules: unit (b, h), granule j of its nt. `left` is what
+// remains of the warp's share, this granule included; nothing if it is not positive.
 struct Cursor {
     int b, h, j, nt;
     int slot, n;
+    long long left;
 
     template <int GR>
     __device__ __forceinline__ void at_row(const PagedCache &c, int row)
@@ -146,19 +129,20 @@ struct Cursor {
         n = slot < 0 ? -1 : length_of(c, slot);
         nt = n < 0 ? 0 : n / GR + 1;
     }
-};
 
-template <int GR>
-__device__ __forceinline__ void advance(const PagedStep &a, Cursor &c, long long left)
-{
-    if (++c.j < c.nt) return;
-    c.j = 0;
-    if (++c.h < a.H) return;
-    c.h = 0;
-    if (left <= 0) return;  // no tile follows in this share
-    do c.at_row<GR>(a.c, c.b + 1);
-    while (c.nt == 0);
-}
+    template <int GR>
+    __device__ __forceinline__ void advance(const PagedStep &a)
+    {
+        --left;
+        if (++j < nt) return;
+        j = 0;
+        left -= UNIT_COST;
+        if (left <= 0 || ++h < a.H) return;
+        h = 0;
+        do at_row<GR>(a.c, b + 1);  // a row with granules follows, for something is left
+        while (nt == 0);
+    }
+};
 
 // A unit's piece that a warp does not hold whole, for the block to put together.
 template <int D>
@@ -176,9 +160,9 @@ __global__ void __launch_bounds__(NT, 1) decode_own_kernel(PagedStep a, PagedScr
     constexpr int LPR = C::LPR, RPP = C::RPP, GR = C::GR, CPL = C::CPL, S = C::STAGES;
     constexpr int VP = Vec<T>::N / 2;  // pairs of a chunk
     extern __shared__ __align__(128) char smem[];
+    long long *s_cum = reinterpret_cast<long long *>(smem);  // before the rings are filled
     __shared__ uint64_t s_bar[WARPS][S];
     __shared__ long long s_row[WARPS][S];  // first row of the stage's granule in the pool, or -1
-    __shared__ long long s_cum[NT];
     __shared__ Piece<D> s_piece[WARPS][2];
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int lr = lane % LPR, grp = lane / LPR;
@@ -193,12 +177,14 @@ __global__ void __launch_bounds__(NT, 1) decode_own_kernel(PagedStep a, PagedScr
     }
     if (blockIdx.x == 0 && tid == 0) *s.err = 0;
 
-    // this warp's share [t0, t1) of all tiles, and the batch row that t0 lies in. No more warps
-    // than tiles take part, so no share is empty and the blocks of a unit follow one another.
+    // this warp's share [t0, t1) of all cost, and the batch row that t0 lies in. A unit's cost
+    // comes before its granules: a share that ends in it holds none of the unit's granules, one
+    // that starts in it starts with its first. No share is empty, so the blocks between the
+    // first and the last that hold granules of a unit hold some too.
     long long total = 0, mine = 0, at = 0;
     for (int b0 = 0; b0 < a.B; b0 += NT) {
         long long sum;
-        mine = b0 + tid < a.B ? (long long)tiles_of<GR>(c, b0 + tid) * a.H : 0;
+        mine = b0 + tid < a.B ? (long long)cost_of<GR>(c, b0 + tid) * a.H : 0;
         at = block_scan(mine, &sum);
         total += sum;
     }
@@ -210,7 +196,7 @@ __global__ void __launch_bounds__(NT, 1) decode_own_kernel(PagedStep a, PagedScr
     for (int b0 = 0; b0 < a.B; b0 += NT) {
         long long sum = total;
         if (a.B > NT) {
-            mine = b0 + tid < a.B ? (long long)tiles_of<GR>(c, b0 + tid) * a.H : 0;
+            mine = b0 + tid < a.B ? (long long)cost_of<GR>(c, b0 + tid) * a.H : 0;
             at = block_scan(mine, &sum);
         }
         s_cum[tid] = cum + at;
@@ -226,23 +212,29 @@ __global__ void __launch_bounds__(NT, 1) decode_own_kernel(PagedStep a, PagedScr
             }
             cc.at_row<GR>(c, b0 + lo);
             const long long off = t0 - s_cum[lo];
-            cc.h = (int)(off / cc.nt);
-            cc.j = (int)(off % cc.nt);
+            const int at_unit = (int)(off % (cc.nt + UNIT_COST)) - UNIT_COST;
+            cc.h = (int)(off / (cc.nt + UNIT_COST));
+            cc.j = max(0, at_unit);
+            cc.left = t1 - t0 + min(0, at_unit);
         }
         cum += sum;
         __syncthreads();
     }
+    tc::fence_async_smem();  // s_cum's place now belongs to the copies
 
-    if (t0 < t1) {
+    if (cc.left > 0) {
         const float scale2 = a.scale * LOG2E;
-        char *ring = smem + warp * C::RING;
-        float *gring = reinterpret_cast<float *>(smem + WARPS * C::RING) + warp * S * GR;
+        char *ring = smem + warp * C::RING, *head = smem + WARPS * C::RING + warp * C::HEAD;
+        float *gring = reinterpret_cast<float *>(smem + WARPS * (C::RING + C::HEAD)) + warp * S * GR;
         T *K = static_cast<T *>(c.k), *Vp = static_cast<T *>(c.v);
 
-        // the loads run ahead of the arithmetic by S granules
+        // The loads run ahead of the arithmetic by S granules, across units: a unit's first granule
+        // brings q and w along (beta and log f wait in the stage's lane), its last one the new
+        // token, which lands in the tile at its row.
         Cursor pc = cc;
         int tab_b = -1, tab_at = 0, tab = -1;  // 32 entries of row tab_b's table, one a lane
-        long long tp = t0;
+        bool begun = false;
+        float p_beta = 0.f, p_lf = 0.f;
         auto load = [&](int st) {
             const int r0 = pc.j * GR, pg = r0 >> c.page_log2;
             if (pc.b != tab_b || pg < tab_at || pg >= tab_at + 32) {
@@ -252,51 +244,74 @@ __global__ void __launch_bounds__(NT, 1) decode_own_kernel(PagedStep a, PagedScr
                 tab = i < c.max_pages ? c.table[(long long)pc.slot * c.max_pages + i] : -1;
             }
             const int p = __shfl_sync(0xffffffffu, tab, pg - tab_at);
-            const bool ok = p >= 0 && p < c.n_pages;
+            const bool ok = p >= 0 && p < c.n_pages, opens = pc.j == 0 || !begun;
             const long long row = ((long long)p * a.H + pc.h) * page + (r0 & (page - 1));
+            const long long pu = (long long)pc.b * a.H + pc.h;
+            if (opens && lane == st) {
+                p_beta = a.beta[pu];
+                if (GATE) p_lf = a.log_f[pu];
+            }
             if (lane == 0) {
                 s_row[warp][st] = ok ? row : -1;
                 uint64_t *bar = &s_bar[warp][st];
-                if (ok) {
-                    tc::mbar_expect_tx(bar, 2 * C::TILE + (GATE ? C::GATE : 0));
-                    tc::bulk_load(ring + st * 2 * C::TILE, K + row * D, C::TILE, bar);
-                    tc::bulk_load(ring + st * 2 * C::TILE + C::TILE, Vp + row * D, C::TILE, bar);
-                    if (GATE) tc::bulk_load(gring + st * GR, c.g + row, C::GATE, bar);
-                } else {
+                const int have = min(GR, pc.n - r0);  // cached rows of this granule
+                const bool fresh = have < GR;
+                const uint32_t bytes = have * C::ROW;
+                char *tk = ring + st * 2 * C::TILE, *tv = tk + C::TILE;
+                const uint32_t tx = (opens ? 2 * C::ROW : 0) +
+                                    (ok ? 2 * bytes + (fresh ? 2 * C::ROW : 0) + (GATE ? C::GATE : 0) : 0);
+                if (tx)
+                    tc::mbar_expect_tx(bar, tx);
+                else
                     tc::mbar_arrive(bar);
+                if (opens) {
+                    tc::bulk_load(head + st * 2 * C::ROW, static_cast<const T *>(a.q) + pu * D, C::ROW, bar);
+                    tc::bulk_load(head + st * 2 * C::ROW + C::ROW, static_cast<const T *>(a.w) + pu * D, C::ROW, bar);
+                }
+                if (ok) {
+                    if (bytes) {
+                        tc::bulk_load(tk, K + row * D, bytes, bar);
+                        tc::bulk_load(tv, Vp + row * D, bytes, bar);
+                    }
+                    if (fresh) {
+                        tc::bulk_load(tk + bytes, static_cast<const T *>(a.k_new) + pu * D, C::ROW, bar);
+                        tc::bulk_load(tv + bytes, static_cast<const T *>(a.v_new) + pu * D, C::ROW, bar);
+                    }
+                    if (GATE) tc::bulk_load(gring + st * GR, c.g + row, C::GATE, bar);
                 }
             }
-            ++tp;
-            advance<GR>(a, pc, t1 - tp);
+            begun = true;
+            pc.advance<GR>(a);
         };
-        for (int i = 0; i < S && tp < t1; ++i) load(i);
+        for (int i = 0; i < S && pc.left > 0; ++i) load(i);
 
         int st = 0, parity = 0, flags = 0, npiece = 0, u = -1, tb = 0;
         bool dead = false;
         float beta = 0.f, lf = 0.f, m = -INFINITY, l = 0.f;
         F2 q[8], w[8], acc[8];
-        for (long long t = t0; t < t1; ++t) {
+        while (cc.left > 0) {
+            if (!tc::mbar_wait(&s_bar[warp][st], parity, dead ? 0 : tc::WAIT_LIMIT_NS)) dead = true;
+            dead = __any_sync(0xffffffffu, dead);
+            const long long row0 = s_row[warp][st];
+            const int r0 = cc.j * GR, n = cc.n;
             if (u != cc.b * a.H + cc.h) {  // a new unit
                 u = cc.b * a.H + cc.h;
                 tb = cc.j;
                 flags = 0;
-                beta = a.beta[u];
-                if (GATE) lf = a.log_f[u];
+                beta = __shfl_sync(0xffffffffu, p_beta, st);
+                if (GATE) lf = __shfl_sync(0xffffffffu, p_lf, st);
+                const uint4 *hq = reinterpret_cast<const uint4 *>(head + st * 2 * C::ROW);
 #pragma unroll
                 for (int j = 0; j < CPL; ++j) {
-                    const long long x = (long long)u * C::ROW_CHUNKS + lr + LPR * (j ^ odd);
-                    to_pairs<T>(static_cast<const uint4 *>(a.q)[x], q + j * VP);
-                    to_pairs<T>(static_cast<const uint4 *>(a.w)[x], w + j * VP);
+                    const int x = lr + LPR * (j ^ odd);
+                    to_pairs<T>(hq[x], q + j * VP);
+                    to_pairs<T>(hq[C::ROW_CHUNKS + x], w + j * VP);
                 }
                 m = -INFINITY;
                 l = 0.f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) acc[i] = 0ull;
             }
-            if (!tc::mbar_wait(&s_bar[warp][st], parity, dead ? 0 : tc::WAIT_LIMIT_NS)) dead = true;
-            dead = __any_sync(0xffffffffu, dead);
-            const long long row0 = s_row[warp][st];
-            const int r0 = cc.j * GR, n = cc.n;
             if (dead) flags |= GAVE_UP;
             if (row0 < 0) flags |= BAD_PAGE;
             const uint4 *tk = reinterpret_cast<const uint4 *>(ring + st * 2 * C::TILE);
@@ -313,8 +328,7 @@ __global__ void __launch_bounds__(NT, 1) decode_own_kernel(PagedStep a, PagedScr
 #pragma unroll
                     for (int j = 0; j < CPL; ++j) {
                         const int x = lr + LPR * (j ^ odd);
-                        kc[j] = fresh ? static_cast<const uint4 *>(a.k_new)[(long long)u * C::ROW_CHUNKS + x]
-                                      : tk[ri * C::ROW_CHUNKS + x];
+                        kc[j] = tk[ri * C::ROW_CHUNKS + x];
                         to_pairs<T>(kc[j], k + j * VP);
                     }
                     const float nc = -(beta * group_sum<LPR>(dot16(w, k)));
@@ -360,12 +374,8 @@ __global__ void __launch_bounds__(NT, 1) decode_own_kernel(PagedStep a, PagedScr
                     for (int j = 0; j < CPL; ++j) {
                         const int x = lr + LPR * (j ^ odd);
                         uint4 vc = make_uint4(0u, 0u, 0u, 0u);  // a row behind the last counts nothing
-                        if (fresh) {
-                            vc = static_cast<const uint4 *>(a.v_new)[(long long)u * C::ROW_CHUNKS + x];
-                            reinterpret_cast<uint4 *>(Vp + (row0 + ri) * D)[x] = vc;
-                        } else if (valid) {
-                            vc = tv[ri * C::ROW_CHUNKS + x];
-                        }
+                        if (valid) vc = tv[ri * C::ROW_CHUNKS + x];
+                        if (fresh) reinterpret_cast<uint4 *>(Vp + (row0 + ri) * D)[x] = vc;
                         F2 v[VP];
                         to_pairs<T>(vc, v);
 #pragma unroll
@@ -380,7 +390,7 @@ __global__ void __launch_bounds__(NT, 1) decode_own_kernel(PagedStep a, PagedScr
                     granule(std::false_type{});
             }
             __syncwarp();  // the stage has been read
-            if (tp < t1 && !dead) load(st);
+            if (pc.left > 0 && !dead) load(st);
             if (++st == S) {
                 st = 0;
                 parity ^= 1;
@@ -388,7 +398,8 @@ __global__ void __launch_bounds__(NT, 1) decode_own_kernel(PagedStep a, PagedScr
             const bool ends = cc.j + 1 == cc.nt;
             const int u_done = u;
             const bool whole = ends && tb == 0;
-            if (ends || t + 1 == t1) {  // the row groups join; then lanes 0 .. LPR - 1 hold the row
+            cc.advance<GR>(a);
+            if (ends || cc.left <= 0) {  // the row groups join; then lanes 0 .. LPR - 1 hold the row
                 float M = m;
 #pragma unroll
                 for (int o = LPR; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
@@ -467,7 +478,6 @@ __global__ void __launch_bounds__(NT, 1) decode_own_kernel(PagedStep a, PagedScr
                     }
                 }
             }
-            advance<GR>(a, cc, t1 - t - 1);
         }
         if (dead)  // copies may still be on their way into this block's memory
             for (int i = 0; i < S; ++i)
@@ -552,7 +562,7 @@ __global__ void __launch_bounds__(D) decode_join_kernel(PagedStep a, PagedScratc
         const long long total = (long long)p.pre_units * p.key_tiles, t0 = pu * p.key_tiles;
         j0 = (int)(((t0 + 1) * p.pre_blocks - 1) / total);
         j1 = (int)(((t0 + p.key_tiles) * p.pre_blocks - 1) / total);
-        for (int j = j0; j <= j1; ++j) flag |= s.pre_flag[j + pu];
+        for (int j = j0; j <= j1; ++j) flag |= s.pre_flag[2 * (j + pu)] | s.pre_flag[2 * (j + pu) + 1];
     }
     flag &= BAD_PAGE | GAVE_UP;
     if (flag && e == 0) atomicMax(s.err, flag & BAD_PAGE ? ERR_PAGE : ERR_PAGED_WAIT);
@@ -614,10 +624,11 @@ PagedPlan paged_plan(int B, int H, int max_pages, int page, int d, int dt, int p
     const long long blocks = (most + WARPS - 1) / WARPS;
     p.own_blocks = (int)(blocks < sms ? blocks : sms);
     p.own_slots = p.own_blocks + B * H;
-    // bf16: the prefix is read once for 64 queries, or for 32 with half the softmax; fp32: CUDA cores
-    p.q_tile = dt == BF16 && B > 32 ? 64 : 32;
-    p.key_tile = dt == BF16 ? 128 : 64;
+    // bf16: the prefix is read once for up to 64 queries, tiles of even size (their softmax is what
+    // can take longer than the loads); fp32: tiles of the CUDA-core kernel
+    p.q_tile = dt == BF16 ? ceil_div(ceil_div(B, ceil_div(B, 64)), 16) * 16 : 32;
     p.q_tiles = ceil_div(B, p.q_tile);
+    p.key_tile = dt == BF16 ? 128 : 64;
     p.key_tiles = (int)(((long long)prefix_len + p.key_tile - 1) / p.key_tile);
     p.pre_units = p.q_tiles * H;
     const long long tiles = (long long)p.pre_units * p.key_tiles;
@@ -638,9 +649,10 @@ size_t paged_carve(void *base, const PagedPlan &p, int B, int H, int d, PagedScr
     s.own_flag = c.take<int>(own);
     s.qt = c.take<float>((size_t)p.q_tiles * p.q_tile * H * d);
     s.qg = c.take<float>((size_t)p.q_tiles * p.q_tile * H);
-    s.pre = c.take<float>(pre * p.q_tile * d);
-    s.pre_ml = c.take<float>(pre * 2 * p.q_tile);
-    s.pre_flag = c.take<int>(pre);
+    // room for the largest tile, so that a larger batch never needs less
+    s.pre = c.take<float>(pre * 64 * d);
+    s.pre_ml = c.take<float>(pre * 2 * 64);
+    s.pre_flag = c.take<int>(2 * pre);
     return c.bytes();
 }
 

@@ -16,15 +16,18 @@
 // multiplied twice; the tensor cores have the time (see the tile costs below).
 //
 // The running maximum of a query is a reference that moves only when a logit
-// passes it by more than 2^8 (or at a unit's first tile): then all four warps
-// agree on the new one and O^T is scaled in tensor memory. Otherwise a tile
+// passes it by more than 2^8 (or at a unit's first tile): then the warps that
+// hold the query agree on the new one and O^T is scaled in tensor memory. Otherwise a tile
 // needs no maximum across threads at all: weights stay below 2^8 and sums and
 // products are fp32. A thread keeps the sum of its own keys' weights per query;
 // they are added up across threads at a unit's end.
 //
-// Warps 0-3 softmax, 4 loads (a box of min(page, 128) rows a page, TMA), 5 MMA.
+// Warps 0-3 and 4-7 softmax, one half of the queries each (they share nothing but the
+// barriers towards the MMAs; with four warps for all queries the softmax of a tile took
+// longer than its loads), 8 loads (a box of min(page, 128) rows a page, TMA), 9 MMA.
 // Waits are bounded; one that gives up makes its pieces NaN and is reported.
 #include "paged.cuh"
+#include "rowvec.cuh"
 #include "runtime.cuh"
 #include "tc.cuh"
 
@@ -34,7 +37,7 @@ namespace {
 
 using namespace tc;
 
-constexpr int NT = 192, NSOFT = 128, W_LOAD = 4, W_MMA = 5;
+constexpr int NT = 320, NSOFT = 256, W_LOAD = 8, W_MMA = 9;
 constexpr int KT = 128;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LOW = -1e30f;  // reference of a query that has no weight yet
@@ -57,16 +60,17 @@ struct Cfg {
     static_assert(SMEM <= 232448, "shared memory");
 };
 
-__device__ __forceinline__ void soft_bar() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// Barriers of one half of the softmax warps.
+__device__ __forceinline__ void half_bar(int half) { asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory"); }
 
-__device__ __forceinline__ bool soft_any(bool x)
+__device__ __forceinline__ bool half_any(int half, bool x)
 {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}\n"
+        "barrier.cta.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}\n"
         : "=r"(r)
-        : "r"((uint32_t)x)
+        : "r"((uint32_t)x), "r"(1 + half)
         : "memory");
     return r != 0;
 }
@@ -78,20 +82,34 @@ __device__ __forceinline__ float warp_max(float x)
     return r;
 }
 
-// Sum over the warp's lanes of each of 32 values; lane i gets the i-th.
-__device__ __forceinline__ float warp_sums(float (&v)[32])
+// Sum over the warp's lanes of each of N values; lane i gets the i % N-th.
+template <int N>
+__device__ __forceinline__ float warp_sums(float (&v)[N])
 {
     const int lane = threadIdx.x % 32;
 #pragma unroll
-    for (int o = 16, n = 16; o > 0; o >>= 1, n >>= 1) {
+    for (int o = 16; o >= N; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+#pragma unroll
+    for (int o = N / 2; o > 0; o >>= 1) {
         const bool up = lane & o;
 #pragma unroll
-        for (int i = 0; i < n; ++i) {
-            const float send = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
+        for (int i = 0; i < o; ++i) {
+            const float send = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
             v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
         }
     }
     return v[0];
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_cols(uint32_t taddr, float (&v)[N])
+{
+    if constexpr (N == 32)
+        tmem_ld32(taddr, v);
+    else
+        tmem_ld16_wait(taddr, v);
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
@@ -150,7 +168,7 @@ __global__ void __launch_bounds__(NT, 1)
     const long long total = (long long)p.pre_units * p.key_tiles;
     const long long t0 = total * blockIdx.x / gridDim.x, t1 = total * (blockIdx.x + 1) / gridDim.x;
     const int count = (int)(t1 - t0);
-    const int q_rows = p.q_tiles * QN;
+    const int QT = p.q_tile, q_rows = p.q_tiles * QT;  // queries of a unit: a multiple of 16, at most QN
 
     if (warp == W_LOAD) {
         const int log2p = a.c.page_log2, page = 1 << log2p, box = page < KT ? page : KT, boxes = KT / box;
@@ -167,8 +185,8 @@ __global__ void __launch_bounds__(NT, 1)
                     break;
                 }
                 if (lane == 0) {
-                    mbar_expect_tx(q_full, C::Q);
-                    const int row = h * q_rows + (u % p.q_tiles) * QN;
+                    mbar_expect_tx(q_full, 2 * QT * D * 2);
+                    const int row = h * q_rows + (u % p.q_tiles) * QT;
                     for (int x = 0; x < PANELS; ++x) {
                         tma_load_2d(sm + C::Q_OFF + x * QN * 128, &mQ, 64 * x, row, q_full);
                         tma_load_2d(sm + C::Q_OFF + (PANELS + x) * QN * 128, &mQ, 64 * x, a.H * q_rows + row, q_full);
@@ -236,7 +254,7 @@ __global__ void __launch_bounds__(NT, 1)
         if (lane == 0) {
             // Tile costs at D = 128 in tensor-core cycles: S^T 8 steps x 2 (hi, lo) x 32, O^T
             // the same, 1024 in all, where the loads of a tile take 2800.
-            constexpr uint32_t idS = idesc_f16(128, QN, AB_BF16, 0, 0), idO = idesc_f16(D, 64, AB_BF16, 1, 1);
+            const uint32_t idS = idesc_f16(128, QT, AB_BF16, 0, 0), idO = idesc_f16(D, QN == 32 ? 64 : QT, AB_BF16, 1, 1);
             const uint32_t q_addr = smem_u32(sm + C::Q_OFF), p_addr = smem_u32(sm + C::P_OFF);
             int seg = 0;
             bool ok = true;
@@ -287,10 +305,12 @@ __global__ void __launch_bounds__(NT, 1)
             mbar_wait(mma_done, 0, 8 * WAIT_LIMIT_NS);
         }
     } else {
-        // thread = key of the tile (a lane of S^T), then a row of O^T: dim tid, or at D = 64
-        // dim 16 warp + lane in the lanes below 16
-        const uint32_t lane_off = (uint32_t)(32 * warp) << 16;
-        const float scale2 = a.scale * LOG2E;
+        // thread = key of the tile (a lane of S^T), columns c0 .. c0 + CG - 1 of its half of the
+        // queries; then a row of O^T: dim ht, or at D = 64 dim 16 (warp % 4) + lane in the lanes below 16
+        constexpr int CN = QN / 2;
+        const int half = warp / 4, ht = tid % 128, CG = QT / 2, c0 = half * CG;
+        const uint32_t lane_off = (uint32_t)(32 * (warp % 4)) << 16;
+        const F2 scale2 = f2(a.scale * LOG2E, a.scale * LOG2E);
         uint8_t *sP = sm + C::P_OFF;
         bool ok = true;
         int n = 0;
@@ -299,133 +319,136 @@ __global__ void __launch_bounds__(NT, 1)
             const int u = (int)(t / p.key_tiles), kb = (int)(t % p.key_tiles);
             const int ke = (int)min((long long)p.key_tiles, kb + (t1 - t));
             const int qt = u % p.q_tiles, h = u / p.q_tiles;
-            const int nq = min(QN, a.B - qt * QN);  // queries of this unit
-            float l[QN];
+            const int nq = min(CG, a.B - qt * QT - c0);  // queries of this unit and half
+            F2 l[CN / 2];
 #pragma unroll
-            for (int i = 0; i < QN; ++i) l[i] = 0.f;
+            for (int i = 0; i < CN / 2; ++i) l[i] = 0ull;
             for (int kt = kb; kt < ke; ++kt, ++n) {
-                const bool first = kt == kb;
-                const bool live = kt * KT + tid < a.prefix_len;
+                const bool first = kt == kb, tail = (kt + 1) * KT > a.prefix_len;
+                const bool live = !tail || kt * KT + ht < a.prefix_len;
                 if (ok && !mbar_wait(&s_full[n & 1], (n >> 1) & 1, WAIT_LIMIT_NS)) ok = false;
                 float g = 0.f;
                 if (gate) {
                     if (ok && !mbar_wait(&g_full[n % NG], (n / NG) & 1, WAIT_LIMIT_NS)) ok = false;
-                    if (ok) g = sG[(n % NG) * KT + tid] * LOG2E;
+                    if (ok) g = sG[(n % NG) * KT + ht] * LOG2E;
                 }
                 ok = __all_sync(0xffffffffu, ok);
                 fence_after_sync();
-                float z[QN];
-                auto logits = [&](int c) {  // columns c .. c + 31
-                    float v[32];
-                    tmem_ld32(tbase + C::T_S + (n & 1) * QN + c + lane_off, v);
+                F2 z[CN / 2];
+                const F2 g2 = f2(g, g);
+                auto logits = [&]() {
+                    float v[CN];
+                    tmem_cols<CN>(tbase + C::T_S + (n & 1) * QN + c0 + lane_off, v);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) z[c + i] = live ? fmaf(v[i], scale2, g) : -INFINITY;
+                    for (int i = 0; i < CN / 2; ++i) z[i] = fma2(f2(v[2 * i], v[2 * i + 1]), scale2, g2);
+                    if (!live) {  // the page's rows behind the prefix hold anything
+#pragma unroll
+                        for (int i = 0; i < CN / 2; ++i) z[i] = f2(-INFINITY, -INFINITY);
+                    }
                 };
-                auto minus_ref = [&](int c) {
+                auto minus_ref = [&]() {
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4) {
-                        const float4 m = *reinterpret_cast<const float4 *>(sM + c + i);
-                        z[c + i] -= m.x;
-                        z[c + i + 1] -= m.y;
-                        z[c + i + 2] -= m.z;
-                        z[c + i + 3] -= m.w;
+                    for (int i = 0; i < CN / 2; i += 2) {
+                        const ulonglong2 m = *reinterpret_cast<const ulonglong2 *>(sM + c0 + 2 * i);
+                        z[i] = add2(z[i], m.x);
+                        z[i + 1] = add2(z[i + 1], m.y);
                     }
                 };
                 float top = -INFINITY;
-                if (ok) {
+                if (ok && nq > 0) {
+                    logits();
+                    if (!first) {
+                        minus_ref();
 #pragma unroll
-                    for (int c = 0; c < QN; c += 32) {
-                        if (c >= nq) break;
-                        logits(c);
-                        if (!first) {
-                            minus_ref(c);
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) top = fmaxf(top, z[c + i]);
+                        for (int i = 0; i < CN / 2; ++i) {
+                            float x, y;
+                            split(z[i], x, y);
+                            if (2 * i < nq) top = fmaxf(top, fmaxf(x, y));
                         }
                     }
                 }
                 // P's buffer and O^T are free once the former tile's product is done
                 if (ok && n > 0 && !mbar_wait(o_done, (n - 1) & 1, WAIT_LIMIT_NS)) ok = false;
                 ok = __all_sync(0xffffffffu, ok);
-                if (soft_any(first || top > SLACK)) {
-                    if (ok) {
+                if (half_any(half, first || top > SLACK)) {
+                    if (ok && nq > 0) {
                         fence_after_sync();
+                        logits();
+                        float mine = -INFINITY;
 #pragma unroll
-                        for (int c = 0; c < QN; c += 32) {
-                            if (c >= nq) break;
-                            logits(c);
-                            float mine = -INFINITY;
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) {
-                                const float x = warp_max(z[c + i]);
-                                if (lane == i) mine = x;
-                            }
-                            sR[warp * QN + c + lane] = mine;
+                        for (int i = 0; i < CN / 2; ++i) {
+                            float x, y;
+                            split(z[i], x, y);
+                            x = warp_max(x);
+                            y = warp_max(y);
+                            if (lane == 2 * i) mine = x;
+                            if (lane == 2 * i + 1) mine = y;
                         }
+                        if (lane < CG) sR[(warp % 4) * QN + c0 + lane] = mine;
                     }
-                    soft_bar();
-                    if (tid < QN) {
-                        const float old = first ? -INFINITY : sM[tid];
-                        float x = fmaxf(fmaxf(sR[tid], sR[QN + tid]), fmaxf(sR[2 * QN + tid], sR[3 * QN + tid]));
+                    half_bar(half);
+                    if (ht < CG) {
+                        const int c = c0 + ht;
+                        const float old = first ? -INFINITY : -sM[c];
+                        float x = fmaxf(fmaxf(sR[c], sR[QN + c]), fmaxf(sR[2 * QN + c], sR[3 * QN + c]));
                         x = fmaxf(fmaxf(old, x), LOW);
-                        sM[tid] = x;
-                        sF[tid] = ex2(old - x);
+                        sM[c] = -x;
+                        sF[c] = ex2(old - x);
                     }
-                    soft_bar();
-                    if (ok) {
+                    half_bar(half);
+                    if (ok && nq > 0) {
                         if (!first) {
 #pragma unroll
-                            for (int i = 0; i < QN; ++i) l[i] *= sF[i];
+                            for (int i = 0; i < CN / 2; ++i)
+                                if (2 * i < CG) l[i] = mul2(l[i], f2(sF[c0 + 2 * i], sF[c0 + 2 * i + 1]));
 #pragma unroll 1
-                            for (int c = 0; c < 64; c += 32) {
-                                float v[32];
-                                tmem_ld32(tbase + C::T_O + c + lane_off, v);
+                            for (int part = 0; part < 64 / QN; ++part) {  // at 32 queries hi and lo
+                                const uint32_t at = tbase + C::T_O + part * 32 + c0 + lane_off;
+                                float v[CN];
+                                tmem_cols<CN>(at, v);
 #pragma unroll
-                                for (int i = 0; i < 32; i += 8) {
+                                for (int i = 0; i < CN; i += 8) {
+                                    if (i >= CG) break;
                                     uint32_t r[8];
 #pragma unroll
-                                    for (int e = 0; e < 8; ++e)
-                                        r[e] = __float_as_uint(v[i + e] * sF[(QN == 32 ? 0 : c) + i + e]);
-                                    tmem_st8(tbase + C::T_O + c + i + lane_off, r);
+                                    for (int e = 0; e < 8; ++e) r[e] = __float_as_uint(v[i + e] * sF[c0 + i + e]);
+                                    tmem_st8(at + i, r);
                                 }
                             }
                             tmem_wait_st();
                         }
-#pragma unroll
-                        for (int c = 0; c < QN; c += 32) {
-                            if (c >= nq) break;
-                            minus_ref(c);
-                        }
+                        minus_ref();
                     }
                 }
                 if (ok) {
                     // weights, split in two bf16 numbers; this thread's key is a row of P
+                    const F2 minus1 = f2(-1.f, -1.f);
 #pragma unroll
-                    for (int c = 0; c < QN; c += 32) {
-                        if (c >= nq) break;
+                    for (int i = 0; i < CN; i += 8) {
+                        if (i >= nq) break;
+                        uint32_t hi[4], lo[4];
 #pragma unroll
-                        for (int i = 0; i < 32; i += 8) {
-                            uint32_t hi[4], lo[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const float x = ex2(z[c + i + 2 * e]), y = ex2(z[c + i + 2 * e + 1]);
-                                l[c + i + 2 * e] += x;
-                                l[c + i + 2 * e + 1] += y;
-                                hi[e] = pack_bf16(x, y);
-                                lo[e] = pack_bf16(x - __uint_as_float(hi[e] << 16),
-                                                  y - __uint_as_float(hi[e] & 0xffff0000u));
-                            }
-                            *reinterpret_cast<uint4 *>(sP + sw128_offset(tid, c + i)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                            uint8_t *low = QN == 32 ? sP + sw128_offset(tid, 32 + i) : sP + C::PP + sw128_offset(tid, c + i);
-                            *reinterpret_cast<uint4 *>(low) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        for (int e = 0; e < 4; ++e) {
+                            float x, y;
+                            split(z[i / 2 + e], x, y);
+                            x = ex2(x);
+                            y = ex2(y);
+                            const F2 xy = f2(x, y);
+                            l[i / 2 + e] = add2(l[i / 2 + e], xy);
+                            hi[e] = pack_bf16(x, y);
+                            split(fma2(f2(__uint_as_float(hi[e] << 16), __uint_as_float(hi[e] & 0xffff0000u)), minus1, xy), x, y);
+                            lo[e] = pack_bf16(x, y);
                         }
+                        *reinterpret_cast<uint4 *>(sP + sw128_offset(ht, c0 + i)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        uint8_t *low = QN == 32 ? sP + sw128_offset(ht, 32 + c0 + i) : sP + C::PP + sw128_offset(ht, c0 + i);
+                        *reinterpret_cast<uint4 *>(low) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     }
                     // values behind the prefix's end are whatever the page holds, and are weighed
                     // with zero: make them zero too
-                    if ((kt + 1) * KT > a.prefix_len) {
+                    if (tail && half == 0) {
                         if (!mbar_wait(&v_full[n % NV], (n / NV) & 1, WAIT_LIMIT_NS)) ok = false;
                         if (ok && !live) {
-                            uint8_t *v = sm + C::V_OFF + (n % NV) * C::TILE + tid * 128;
+                            uint8_t *v = sm + C::V_OFF + (n % NV) * C::TILE + ht * 128;
 #pragma unroll
                             for (int x = 0; x < PANELS; ++x)
 #pragma unroll
@@ -444,35 +467,36 @@ __global__ void __launch_bounds__(NT, 1)
             ok = __all_sync(0xffffffffu, ok);
             fence_after_sync();
             const long long piece = (long long)blockIdx.x + u;
-            const int dim = D == 128 ? tid : 16 * warp + lane;
-#pragma unroll
-            for (int c = 0; c < QN; c += 32) {
-                if (c >= nq) break;
-                float v[32], v2[32];
+            if (nq > 0) {
+                const int dim = D == 128 ? ht : 16 * (warp % 4) + lane;
+                float v[CN], v2[CN];
                 if (ok) {
-                    tmem_ld32(tbase + C::T_O + c + lane_off, v);
-                    if (QN == 32) tmem_ld32(tbase + C::T_O + 32 + lane_off, v2);
+                    tmem_cols<CN>(tbase + C::T_O + c0 + lane_off, v);
+                    if (QN == 32) tmem_cols<CN>(tbase + C::T_O + 32 + c0 + lane_off, v2);
                     if (D == 128 || lane < 16) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (c + i < nq) s.pre[(piece * QN + c + i) * D + dim] = QN == 32 ? v[i] + v2[i] : v[i];
+                        for (int i = 0; i < CN; ++i)
+                            if (i < nq) s.pre[(piece * QT + c0 + i) * D + dim] = QN == 32 ? v[i] + v2[i] : v[i];
                     }
                 }
 #pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = l[c + i];
-                sR[warp * QN + c + lane] = warp_sums(v);
+                for (int i = 0; i < CN / 2; ++i) split(l[i], v[2 * i], v[2 * i + 1]);
+                const float sum = warp_sums<CN>(v);
+                if (lane < CG) sR[(warp % 4) * QN + c0 + lane] = sum;
             }
-            const bool failed = soft_any(!ok);
-            if (tid < nq) {
+            const bool failed = half_any(half, !ok);
+            if (ht < nq) {
                 // the gate since the prefix's end weighs every key of it alike; where it leaves
                 // nothing (log f = -inf), neither the sum nor the values count
-                const float M = sM[tid] + s.qg[(long long)h * q_rows + qt * QN + tid];
-                const float L = (sR[tid] + sR[QN + tid]) + (sR[2 * QN + tid] + sR[3 * QN + tid]);
-                s.pre_ml[piece * 2 * QN + tid] = M;
-                s.pre_ml[piece * 2 * QN + QN + tid] = M == -INFINITY && !isnan(L) ? 0.f : L;
+                const int c = c0 + ht;
+                const float M = s.qg[(long long)h * q_rows + qt * QT + c] - sM[c];
+                const float L = (sR[c] + sR[QN + c]) + (sR[2 * QN + c] + sR[3 * QN + c]);
+                s.pre_ml[piece * 2 * QT + c] = M;
+                s.pre_ml[piece * 2 * QT + QT + c] = M == -INFINITY && !isnan(L) ? 0.f : L;
             }
-            if (tid == 0) s.pre_flag[piece] = (failed ? PIECE_GAVE_UP : 0) | (*(volatile int *)s_bad ? PIECE_BAD_PAGE : 0);
-            soft_bar();
+            if (ht == 0)
+                s.pre_flag[2 * piece + half] = (failed ? PIECE_GAVE_UP : 0) | (*(volatile int *)s_bad ? PIECE_BAD_PAGE : 0);
+            half_bar(half);
         }
     }
     fence_before_sync();
@@ -488,7 +512,7 @@ cudaError_t run(const PagedStep &a, const PagedPlan &p, const PagedScratch &s, c
     const int page = 1 << a.c.page_log2;
     const uint64_t rows = (uint64_t)a.c.n_pages * a.H * page;
     CUtensorMap mQ, mK, mV;
-    if (!make_map_2d(&mQ, s.qt, BF16, D, 2ull * a.H * p.q_tiles * QN, QN) ||
+    if (!make_map_2d(&mQ, s.qt, BF16, D, 2ull * a.H * p.q_tiles * p.q_tile, p.q_tile) ||
         !make_map_2d(&mK, a.c.k, BF16, D, rows, page < KT ? page : KT) ||
         !make_map_2d(&mV, a.c.v, BF16, D, rows, page < KT ? page : KT))
         return cudaErrorInvalidValue;
@@ -505,8 +529,8 @@ cudaError_t run(const PagedStep &a, const PagedPlan &p, const PagedScratch &s, c
 cudaError_t prefix_attn_tc(const PagedStep &a, int d, const PagedPlan &p, const PagedScratch &s, cudaStream_t st)
 {
     Stage stage("prefix_attn", st);
-    if (d == 64) return p.q_tile == 32 ? run<64, 32>(a, p, s, st) : run<64, 64>(a, p, s, st);
-    return p.q_tile == 32 ? run<128, 32>(a, p, s, st) : run<128, 64>(a, p, s, st);
+    if (d == 64) return p.q_tile <= 32 ? run<64, 32>(a, p, s, st) : run<64, 64>(a, p, s, st);
+    return p.q_tile <= 32 ? run<128, 32>(a, p, s, st) : run<128, 64>(a, p, s, st);
 }
 
 }  // namespace path

@@ -29,6 +29,9 @@ def test_workspace_sizes(lib):
                  (8, 24, 100, 128, 64, BF16, 0), (8, 24, 100, 64, 64, BF16, 1), (8, 24, 100, 64, 64, F32, 0)):
         assert f(*more) >= base
     assert f(8, 24, 100, 64, 64, BF16, 9000) >= f(8, 24, 100, 64, 64, BF16, 100) > base
+    for dt in (BF16, F32):
+        sizes = [f(b, 24, 100, 64, 128, dt, 5000) for b in range(1, 300)]
+        assert sizes == sorted(sizes)
     for bad in ((0, 1, 1, 16, 64, BF16, 0), (1, 1, 0, 16, 64, BF16, 0), (1, 1, 1, 8, 64, BF16, 0),
                 (1, 1, 1, 48, 64, BF16, 0), (1, 1, 1, 2048, 64, BF16, 0), (1, 1, 1, 16, 96, BF16, 0),
                 (1, 1, 1, 16, 64, MIXED, 0), (1, 1, 1, 16, 64, BF16, -1), (65536, 1, 1, 16, 64, BF16, 0),

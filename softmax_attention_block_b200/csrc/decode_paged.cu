@@ -562,7 +562,7 @@ __global__ void __launch_bounds__(D) decode_join_kernel(PagedStep a, PagedScratc
         const long long total = (long long)p.pre_units * p.key_tiles, t0 = pu * p.key_tiles;
         j0 = (int)(((t0 + 1) * p.pre_blocks - 1) / total);
         j1 = (int)(((t0 + p.key_tiles) * p.pre_blocks - 1) / total);
-        for (int j = j0; j <= j1; ++j) flag |= s.pre_flag[2 * (j + pu)] | s.pre_flag[2 * (j + pu) + 1];
+        for (int j = j0; j <= j1; ++j) flag |= s.pre_flag[4 * (j + pu) + row / 16];
     }
     flag &= BAD_PAGE | GAVE_UP;
     if (flag && e == 0) atomicMax(s.err, flag & BAD_PAGE ? ERR_PAGE : ERR_PAGED_WAIT);
@@ -652,7 +652,7 @@ size_t paged_carve(void *base, const PagedPlan &p, int B, int H, int d, PagedScr
     // room for the largest tile, so that a larger batch never needs less
     s.pre = c.take<float>(pre * 64 * d);
     s.pre_ml = c.take<float>(pre * 2 * 64);
-    s.pre_flag = c.take<int>(2 * pre);
+    s.pre_flag = c.take<int>(4 * pre);
     return c.bytes();
 }
 

@@ -73,7 +73,7 @@ struct PagedScratch {
     float *qg;         // [H, q_rows] the gate's bias since the prefix's end (log2 domain)
     float *pre;        // [pre_slots, q_tile, d] accumulators of the prefix part
     float *pre_ml;     // [pre_slots, 2, q_tile] max (log2 domain) and sum
-    int *pre_flag;     // [pre_slots, 2] PIECE_* (one for each half of the queries)
+    int *pre_flag;     // [pre_slots, 4] PIECE_* (one for each 16 queries)
 };
 
 struct PagedPlan {

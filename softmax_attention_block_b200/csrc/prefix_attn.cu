@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(NT) prefix_simt_kernel(PagedStep a, PagedScrat
                 }
             }
         }
-        if (tid < 2) s.pre_flag[2 * piece + tid] = any_bad ? PIECE_BAD_PAGE : 0;
+        if (tid < 4) s.pre_flag[4 * piece + tid] = any_bad ? PIECE_BAD_PAGE : 0;
         t += ke - kb;
     }
 }

@@ -22,9 +22,10 @@
 // products are fp32. A thread keeps the sum of its own keys' weights per query;
 // they are added up across threads at a unit's end.
 //
-// Warps 0-3 and 4-7 softmax, one half of the queries each (they share nothing but the
-// barriers towards the MMAs; with four warps for all queries the softmax of a tile took
-// longer than its loads), 8 loads (a box of min(page, 128) rows a page, TMA), 9 MMA.
+// Warps: groups of four for the softmax of 16 queries each (they share nothing but the
+// barriers towards the MMAs; the chain of one group, not its instructions, is what a tile
+// waits for, and 16 columns a thread leave room for three or four groups), then one for the
+// loads (a box of min(page, 128) rows a page, TMA) and one for the MMAs.
 // Waits are bounded; one that gives up makes its pieces NaN and is reported.
 #include "paged.cuh"
 #include "rowvec.cuh"
@@ -37,8 +38,8 @@ namespace {
 
 using namespace tc;
 
-constexpr int NT = 320, NSOFT = 256, W_LOAD = 8, W_MMA = 9;
 constexpr int KT = 128;
+constexpr int CN = 16;  // queries of a softmax group
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LOW = -1e30f;  // reference of a query that has no weight yet
 constexpr float SLACK = 8.f;
@@ -46,31 +47,33 @@ constexpr float SLACK = 8.f;
 template <int D, int QN>
 struct Cfg {
     static constexpr int PANELS = D / 64;
+    static constexpr int GROUPS = QN / CN, W_LOAD = 4 * GROUPS, W_MMA = W_LOAD + 1, NT = 32 * (W_MMA + 1);
     static constexpr int TILE = KT * D * 2;             // one operand tile
     static constexpr int NK = D == 64 ? 4 : QN == 32 ? 3 : 2, NV = D == 64 ? 4 : 2, NG = NV + 1;
     static constexpr int Q = 2 * QN * D * 2;            // hi and lo
     static constexpr int PP = KT * 128;                 // one panel of P: 64 columns
     static constexpr int P = QN == 32 ? PP : 2 * PP;    // hi | lo side by side, or a panel each
+    static constexpr int NP = D == 128 && QN == 64 ? 1 : 2;  // buffers of P
     static constexpr int K_OFF = 0, V_OFF = K_OFF + NK * TILE, Q_OFF = V_OFF + NV * TILE, P_OFF = Q_OFF + Q;
-    static constexpr int G_OFF = P_OFF + P, M_OFF = G_OFF + NG * KT * 4, F_OFF = M_OFF + QN * 4;
+    static constexpr int G_OFF = P_OFF + NP * P, M_OFF = G_OFF + NG * KT * 4, F_OFF = M_OFF + QN * 4;
     static constexpr int RED_OFF = F_OFF + QN * 4, BAR_OFF = RED_OFF + 4 * QN * 4;
-    static constexpr int NBAR = 2 * NK + 2 * NV + NG + 7;
+    static constexpr int NBAR = 2 * NK + 2 * NV + NG + 9;
     static constexpr int SMEM = BAR_OFF + NBAR * 8 + 16 + 1024;
-    static constexpr int T_S = 0, T_O = 2 * QN, TMEM = QN == 32 ? 128 : 256;
+    static constexpr int T_S = 0, T_O = 2 * QN, TMEM = 4 * QN;  // two S^T, then O^T for hi | lo
     static_assert(SMEM <= 232448, "shared memory");
 };
 
-// Barriers of one half of the softmax warps.
-__device__ __forceinline__ void half_bar(int half) { asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory"); }
+// Barriers of one softmax group.
+__device__ __forceinline__ void group_bar(int grp) { asm volatile("bar.sync %0, 128;" ::"r"(1 + grp) : "memory"); }
 
-__device__ __forceinline__ bool half_any(int half, bool x)
+__device__ __forceinline__ bool group_any(int grp, bool x)
 {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
         "barrier.cta.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}\n"
         : "=r"(r)
-        : "r"((uint32_t)x), "r"(1 + half)
+        : "r"((uint32_t)x), "r"(1 + grp)
         : "memory");
     return r != 0;
 }
@@ -82,17 +85,14 @@ __device__ __forceinline__ float warp_max(float x)
     return r;
 }
 
-// Sum over the warp's lanes of each of N values; lane i gets the i % N-th.
-template <int N>
-__device__ __forceinline__ float warp_sums(float (&v)[N])
+// Sum over the warp's lanes of each of 16 values; lane i gets the i % 16-th.
+__device__ __forceinline__ float warp_sums(float (&v)[CN])
 {
     const int lane = threadIdx.x % 32;
 #pragma unroll
-    for (int o = 16; o >= N; o >>= 1)
+    for (int i = 0; i < CN; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], 16);
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-#pragma unroll
-    for (int o = N / 2; o > 0; o >>= 1) {
+    for (int o = CN / 2; o > 0; o >>= 1) {
         const bool up = lane & o;
 #pragma unroll
         for (int i = 0; i < o; ++i) {
@@ -103,15 +103,6 @@ __device__ __forceinline__ float warp_sums(float (&v)[N])
     return v[0];
 }
 
-template <int N>
-__device__ __forceinline__ void tmem_cols(uint32_t taddr, float (&v)[N])
-{
-    if constexpr (N == 32)
-        tmem_ld32(taddr, v);
-    else
-        tmem_ld16_wait(taddr, v);
-}
-
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
@@ -119,19 +110,21 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 }
 
 template <int D, int QN>
-__global__ void __launch_bounds__(NT, 1)
+__global__ void __launch_bounds__(Cfg<D, QN>::NT, 1)
     prefix_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
                      const __grid_constant__ CUtensorMap mV, PagedStep a, PagedScratch s, PagedPlan p)
 {
     using C = Cfg<D, QN>;
-    constexpr int NK = C::NK, NV = C::NV, NG = C::NG, PANELS = C::PANELS;
+    constexpr int NK = C::NK, NV = C::NV, NG = C::NG, NP = C::NP, PANELS = C::PANELS;
+    constexpr int W_LOAD = C::W_LOAD, W_MMA = C::W_MMA;
     extern __shared__ uint8_t smraw[];
     uint8_t *sm = smraw + (1024 - (smem_u32(smraw) & 1023)) % 1024;
     uint64_t *k_full = reinterpret_cast<uint64_t *>(sm + C::BAR_OFF), *k_empty = k_full + NK;
     uint64_t *v_full = k_empty + NK, *v_empty = v_full + NV, *g_full = v_empty + NV;
     uint64_t *q_full = g_full + NG, *q_empty = q_full + 1, *s_full = q_full + 2, *p_full = q_full + 4;
-    uint64_t *o_done = q_full + 5, *mma_done = q_full + 6;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(q_full + 7);
+    // P and its product: a barrier for each parity of the tile, since one group may be a tile ahead
+    uint64_t *o_done = q_full + 6, *mma_done = q_full + 8;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(q_full + 9);
     int *s_bad = reinterpret_cast<int *>(tmem_slot + 1);
     float *sG = reinterpret_cast<float *>(sm + C::G_OFF), *sM = reinterpret_cast<float *>(sm + C::M_OFF);
     float *sF = reinterpret_cast<float *>(sm + C::F_OFF), *sR = reinterpret_cast<float *>(sm + C::RED_OFF);
@@ -152,8 +145,10 @@ __global__ void __launch_bounds__(NT, 1)
         mbar_init(q_empty, 1);
         mbar_init(&s_full[0], 1);
         mbar_init(&s_full[1], 1);
-        mbar_init(p_full, NSOFT);
-        mbar_init(o_done, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&p_full[i], p.q_tile / CN * 4);  // a warp each
+            mbar_init(&o_done[i], 1);
+        }
         mbar_init(mma_done, 1);
         mbar_fence_init();
         *s_bad = 0;
@@ -251,86 +246,85 @@ __global__ void __launch_bounds__(NT, 1)
             if (seg > 0) mbar_wait(q_full, (seg - 1) & 1, WAIT_LIMIT_NS);
         }
     } else if (warp == W_MMA) {
-        if (lane == 0) {
-            // Tile costs at D = 128 in tensor-core cycles: S^T 8 steps x 2 (hi, lo) x 32, O^T
-            // the same, 1024 in all, where the loads of a tile take 2800.
-            const uint32_t idS = idesc_f16(128, QT, AB_BF16, 0, 0), idO = idesc_f16(D, QN == 32 ? 64 : QT, AB_BF16, 1, 1);
-            const uint32_t q_addr = smem_u32(sm + C::Q_OFF), p_addr = smem_u32(sm + C::P_OFF);
-            int seg = 0;
+        // The whole warp runs along, converged, and one lane issues: descriptors stay uniform.
+        // A product of 16 keys or dims takes about 72 cycles whatever its other sides are: a tile
+        // has D / 8 of S^T (hi and lo one after the other) and 8 of O^T (hi | lo as columns), 1150 at
+        // D = 64 and 1700 at 128, where its loads take 1400 and 2800.
+        const uint32_t issue = lane == 0;
+        const uint32_t idS = idesc_f16(128, QT, AB_BF16, 0, 0), idO = idesc_f16(D, QN + QT, AB_BF16, 1, 1);
+        const uint32_t q_addr = smem_u32(sm + C::Q_OFF), p_addr = smem_u32(sm + C::P_OFF);
+        int kt = (int)(t0 % p.key_tiles), seg = 0;  // of the S product issued next
+        auto issue_s = [&](int n) -> bool {
+            const int ks = n % NK;
             bool ok = true;
-            auto issue_s = [&](int n) -> bool {
-                const long long t = t0 + n;
-                const int ks = n % NK;
-                if (n == 0 || t % p.key_tiles == 0) {
-                    if (!mbar_wait(q_full, seg & 1, WAIT_LIMIT_NS)) return false;
-                    ++seg;
-                }
-                if (!mbar_wait(&k_full[ks], (n / NK) & 1, WAIT_LIMIT_NS)) return false;
-                fence_after_sync();
-                const uint32_t k_addr = smem_u32(sm + C::K_OFF + ks * C::TILE);
+            if (n == 0 || kt == 0) ok = mbar_wait(q_full, seg++ & 1, WAIT_LIMIT_NS);
+            ok = ok && mbar_wait(&k_full[ks], (n / NK) & 1, WAIT_LIMIT_NS);
+            if (!__all_sync(0xffffffffu, ok)) return false;
+            fence_after_sync();
+            const uint32_t k_addr = smem_u32(sm + C::K_OFF + ks * C::TILE);
 #pragma unroll
-                for (int part = 0; part < 2; ++part)
+            for (int part = 0; part < 2; ++part)
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk)
-                        mma_ss(tbase + C::T_S + (n & 1) * QN,
-                               desc_sw128(k_addr + (kk / 4) * KT * 128 + (kk % 4) * 32, 16, 1024),
-                               desc_sw128(q_addr + (part * PANELS + kk / 4) * QN * 128 + (kk % 4) * 32, 16, 1024),
-                               idS, part + kk > 0);
-                commit(&s_full[n & 1]);
-                commit(&k_empty[ks]);
-                if (n + 1 == count || (t + 1) % p.key_tiles == 0) commit(q_empty);
-                return true;
-            };
-            ok = count > 0 && issue_s(0);
-            for (int n = 0; ok && n < count; ++n) {
-                // the buffer of S(n + 1) was read before P(n - 1) was complete
-                if (n + 1 < count && !issue_s(n + 1)) break;
-                const int vs = n % NV;
-                if (!mbar_wait(&v_full[vs], (n / NV) & 1, WAIT_LIMIT_NS) || !mbar_wait(p_full, n & 1, WAIT_LIMIT_NS)) break;
-                fence_after_sync();
-                const uint32_t v_addr = smem_u32(sm + C::V_OFF + vs * C::TILE);
-                const bool fresh = n == 0 || (t0 + n) % p.key_tiles == 0;
+                for (int kk = 0; kk < D / 16; ++kk)
+                    mma_ss_if(issue, tbase + C::T_S + (n & 1) * QN,
+                              desc_sw128(k_addr + (kk / 4) * KT * 128 + (kk % 4) * 32, 16, 1024),
+                              desc_sw128(q_addr + (part * PANELS + kk / 4) * QN * 128 + (kk % 4) * 32, 16, 1024),
+                              idS, part + kk > 0);
+            commit_if(issue, &s_full[n & 1]);
+            commit_if(issue, &k_empty[ks]);
+            if (++kt == p.key_tiles) kt = 0;
+            if (n + 1 == count || kt == 0) commit_if(issue, q_empty);
+            return true;
+        };
+        bool ok = count > 0 && issue_s(0);
+        int kv = (int)(t0 % p.key_tiles);
+        for (int n = 0; ok && n < count; ++n) {
+            // the buffer of S(n + 1) was read before P(n - 1) was complete
+            if (n + 1 < count && !issue_s(n + 1)) break;
+            const int vs = n % NV;
+            ok = mbar_wait(&v_full[vs], (n / NV) & 1, WAIT_LIMIT_NS) && mbar_wait(&p_full[n & 1], (n >> 1) & 1, WAIT_LIMIT_NS);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            fence_after_sync();
+            const uint32_t v_addr = smem_u32(sm + C::V_OFF + vs * C::TILE);
+            const bool fresh = n == 0 || kv == 0;
+            if (++kv == p.key_tiles) kv = 0;
 #pragma unroll
-                for (int part = 0; part < C::P / C::PP; ++part)
-#pragma unroll
-                    for (int kk = 0; kk < KT / 16; ++kk)
-                        mma_ss(tbase + C::T_O, desc_sw128(v_addr + kk * 2048, KT * 128, 1024),
-                               desc_sw128(p_addr + part * C::PP + kk * 2048, C::PP, 1024), idO,
-                               !fresh || part + kk > 0);
-                commit(&v_empty[vs]);
-                commit(o_done);
-            }
-            // the tensor memory is freed after this warp leaves: no MMA may still be running then
-            commit(mma_done);
-            mbar_wait(mma_done, 0, 8 * WAIT_LIMIT_NS);
+            for (int kk = 0; kk < KT / 16; ++kk)
+                mma_ss_if(issue, tbase + C::T_O, desc_sw128(v_addr + kk * 2048, KT * 128, 1024),
+                          desc_sw128(p_addr + (n % NP) * C::P + kk * 2048, C::PP, 1024), idO, !fresh || kk > 0);
+            commit_if(issue, &v_empty[vs]);
+            commit_if(issue, &o_done[n & 1]);
         }
-    } else {
-        // thread = key of the tile (a lane of S^T), columns c0 .. c0 + CG - 1 of its half of the
-        // queries; then a row of O^T: dim ht, or at D = 64 dim 16 (warp % 4) + lane in the lanes below 16
-        constexpr int CN = QN / 2;
-        const int half = warp / 4, ht = tid % 128, CG = QT / 2, c0 = half * CG;
+        // the tensor memory is freed after this warp leaves: no MMA may still be running then
+        commit_if(issue, mma_done);
+        mbar_wait(mma_done, 0, 8 * WAIT_LIMIT_NS);
+    } else if (warp / 4 * CN < QT) {
+        // thread = key of the tile (a lane of S^T), queries c0 .. c0 + 15; then a row of O^T: dim gt,
+        // or at D = 64 dim 16 (warp % 4) + lane in the lanes below 16
+        const int grp = warp / 4, gt = tid % 128, c0 = grp * CN;
         const uint32_t lane_off = (uint32_t)(32 * (warp % 4)) << 16;
         const F2 scale2 = f2(a.scale * LOG2E, a.scale * LOG2E);
-        uint8_t *sP = sm + C::P_OFF;
         bool ok = true;
         int n = 0;
+        auto product_done = [&](int i) { return mbar_wait(&o_done[i & 1], (i >> 1) & 1, WAIT_LIMIT_NS); };
         while (n < count) {
             const long long t = t0 + n;
             const int u = (int)(t / p.key_tiles), kb = (int)(t % p.key_tiles);
             const int ke = (int)min((long long)p.key_tiles, kb + (t1 - t));
             const int qt = u % p.q_tiles, h = u / p.q_tiles;
-            const int nq = min(CG, a.B - qt * QT - c0);  // queries of this unit and half
+            const int nq = min(CN, a.B - qt * QT - c0);  // queries of this unit and group
             F2 l[CN / 2];
 #pragma unroll
             for (int i = 0; i < CN / 2; ++i) l[i] = 0ull;
             for (int kt = kb; kt < ke; ++kt, ++n) {
                 const bool first = kt == kb, tail = (kt + 1) * KT > a.prefix_len;
-                const bool live = !tail || kt * KT + ht < a.prefix_len;
+                const bool live = !tail || kt * KT + gt < a.prefix_len;
                 if (ok && !mbar_wait(&s_full[n & 1], (n >> 1) & 1, WAIT_LIMIT_NS)) ok = false;
                 float g = 0.f;
                 if (gate) {
                     if (ok && !mbar_wait(&g_full[n % NG], (n / NG) & 1, WAIT_LIMIT_NS)) ok = false;
-                    if (ok) g = sG[(n % NG) * KT + ht] * LOG2E;
+                    if (ok) g = sG[(n % NG) * KT + gt] * LOG2E;
                 }
                 ok = __all_sync(0xffffffffu, ok);
                 fence_after_sync();
@@ -338,7 +332,7 @@ __global__ void __launch_bounds__(NT, 1)
                 const F2 g2 = f2(g, g);
                 auto logits = [&]() {
                     float v[CN];
-                    tmem_cols<CN>(tbase + C::T_S + (n & 1) * QN + c0 + lane_off, v);
+                    tmem_ld16_wait(tbase + C::T_S + (n & 1) * QN + c0 + lane_off, v);
 #pragma unroll
                     for (int i = 0; i < CN / 2; ++i) z[i] = fma2(f2(v[2 * i], v[2 * i + 1]), scale2, g2);
                     if (!live) {  // the page's rows behind the prefix hold anything
@@ -363,14 +357,15 @@ __global__ void __launch_bounds__(NT, 1)
                         for (int i = 0; i < CN / 2; ++i) {
                             float x, y;
                             split(z[i], x, y);
-                            if (2 * i < nq) top = fmaxf(top, fmaxf(x, y));
+                            asm("max.f32 %0, %0, %1, %2;" : "+f"(top) : "f"(x), "f"(y));
                         }
                     }
                 }
-                // P's buffer and O^T are free once the former tile's product is done
-                if (ok && n > 0 && !mbar_wait(o_done, (n - 1) & 1, WAIT_LIMIT_NS)) ok = false;
+                // the buffer of P is free once the product of the tile that had it is done
+                uint8_t *sP = sm + C::P_OFF + (n % NP) * C::P;
+                if (ok && n >= NP && !product_done(n - NP)) ok = false;
                 ok = __all_sync(0xffffffffu, ok);
-                if (half_any(half, first || top > SLACK)) {
+                if (group_any(grp, first || top > SLACK)) {
                     if (ok && nq > 0) {
                         fence_after_sync();
                         logits();
@@ -384,31 +379,33 @@ __global__ void __launch_bounds__(NT, 1)
                             if (lane == 2 * i) mine = x;
                             if (lane == 2 * i + 1) mine = y;
                         }
-                        if (lane < CG) sR[(warp % 4) * QN + c0 + lane] = mine;
+                        if (lane < CN) sR[(warp % 4) * QN + c0 + lane] = mine;
                     }
-                    half_bar(half);
-                    if (ht < CG) {
-                        const int c = c0 + ht;
+                    group_bar(grp);
+                    if (gt < CN) {
+                        const int c = c0 + gt;
                         const float old = first ? -INFINITY : -sM[c];
                         float x = fmaxf(fmaxf(sR[c], sR[QN + c]), fmaxf(sR[2 * QN + c], sR[3 * QN + c]));
                         x = fmaxf(fmaxf(old, x), LOW);
                         sM[c] = -x;
                         sF[c] = ex2(old - x);
                     }
-                    half_bar(half);
+                    group_bar(grp);
+                    if (ok && !first && !product_done(n - 1)) ok = false;
+                    ok = __all_sync(0xffffffffu, ok);
                     if (ok && nq > 0) {
                         if (!first) {
+                            fence_after_sync();
 #pragma unroll
                             for (int i = 0; i < CN / 2; ++i)
-                                if (2 * i < CG) l[i] = mul2(l[i], f2(sF[c0 + 2 * i], sF[c0 + 2 * i + 1]));
+                                l[i] = mul2(l[i], f2(sF[c0 + 2 * i], sF[c0 + 2 * i + 1]));
 #pragma unroll 1
-                            for (int part = 0; part < 64 / QN; ++part) {  // at 32 queries hi and lo
-                                const uint32_t at = tbase + C::T_O + part * 32 + c0 + lane_off;
+                            for (int part = 0; part < 2; ++part) {  // hi, lo
+                                const uint32_t at = tbase + C::T_O + part * QN + c0 + lane_off;
                                 float v[CN];
-                                tmem_cols<CN>(at, v);
+                                tmem_ld16_wait(at, v);
 #pragma unroll
                                 for (int i = 0; i < CN; i += 8) {
-                                    if (i >= CG) break;
                                     uint32_t r[8];
 #pragma unroll
                                     for (int e = 0; e < 8; ++e) r[e] = __float_as_uint(v[i + e] * sF[c0 + i + e]);
@@ -439,16 +436,16 @@ __global__ void __launch_bounds__(NT, 1)
                             split(fma2(f2(__uint_as_float(hi[e] << 16), __uint_as_float(hi[e] & 0xffff0000u)), minus1, xy), x, y);
                             lo[e] = pack_bf16(x, y);
                         }
-                        *reinterpret_cast<uint4 *>(sP + sw128_offset(ht, c0 + i)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                        uint8_t *low = QN == 32 ? sP + sw128_offset(ht, 32 + c0 + i) : sP + C::PP + sw128_offset(ht, c0 + i);
+                        *reinterpret_cast<uint4 *>(sP + sw128_offset(gt, c0 + i)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        uint8_t *low = QN == 32 ? sP + sw128_offset(gt, 32 + c0 + i) : sP + C::PP + sw128_offset(gt, c0 + i);
                         *reinterpret_cast<uint4 *>(low) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     }
                     // values behind the prefix's end are whatever the page holds, and are weighed
                     // with zero: make them zero too
-                    if (tail && half == 0) {
+                    if (tail && grp == 0) {
                         if (!mbar_wait(&v_full[n % NV], (n / NV) & 1, WAIT_LIMIT_NS)) ok = false;
                         if (ok && !live) {
-                            uint8_t *v = sm + C::V_OFF + (n % NV) * C::TILE + ht * 128;
+                            uint8_t *v = sm + C::V_OFF + (n % NV) * C::TILE + gt * 128;
 #pragma unroll
                             for (int x = 0; x < PANELS; ++x)
 #pragma unroll
@@ -458,45 +455,45 @@ __global__ void __launch_bounds__(NT, 1)
                     }
                     fence_async_smem();
                     fence_before_sync();
-                    if (ok) mbar_arrive(p_full);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (ok && lane == 0) mbar_arrive(&p_full[n & 1]);
                 }
-                ok = __all_sync(0xffffffffu, ok);
             }
             // the piece of this unit
-            if (ok && !mbar_wait(o_done, (n - 1) & 1, WAIT_LIMIT_NS)) ok = false;
+            if (ok && !product_done(n - 1)) ok = false;
             ok = __all_sync(0xffffffffu, ok);
             fence_after_sync();
             const long long piece = (long long)blockIdx.x + u;
             if (nq > 0) {
-                const int dim = D == 128 ? ht : 16 * (warp % 4) + lane;
+                const int dim = D == 128 ? gt : 16 * (warp % 4) + lane;
                 float v[CN], v2[CN];
                 if (ok) {
-                    tmem_cols<CN>(tbase + C::T_O + c0 + lane_off, v);
-                    if (QN == 32) tmem_cols<CN>(tbase + C::T_O + 32 + c0 + lane_off, v2);
+                    tmem_ld16_wait(tbase + C::T_O + c0 + lane_off, v);
+                    tmem_ld16_wait(tbase + C::T_O + QN + c0 + lane_off, v2);
                     if (D == 128 || lane < 16) {
 #pragma unroll
                         for (int i = 0; i < CN; ++i)
-                            if (i < nq) s.pre[(piece * QT + c0 + i) * D + dim] = QN == 32 ? v[i] + v2[i] : v[i];
+                            if (i < nq) s.pre[(piece * QT + c0 + i) * D + dim] = v[i] + v2[i];
                     }
                 }
 #pragma unroll
                 for (int i = 0; i < CN / 2; ++i) split(l[i], v[2 * i], v[2 * i + 1]);
-                const float sum = warp_sums<CN>(v);
-                if (lane < CG) sR[(warp % 4) * QN + c0 + lane] = sum;
+                const float sum = warp_sums(v);
+                if (lane < CN) sR[(warp % 4) * QN + c0 + lane] = sum;
             }
-            const bool failed = half_any(half, !ok);
-            if (ht < nq) {
+            const bool failed = group_any(grp, !ok);
+            if (gt < nq) {
                 // the gate since the prefix's end weighs every key of it alike; where it leaves
                 // nothing (log f = -inf), neither the sum nor the values count
-                const int c = c0 + ht;
+                const int c = c0 + gt;
                 const float M = s.qg[(long long)h * q_rows + qt * QT + c] - sM[c];
                 const float L = (sR[c] + sR[QN + c]) + (sR[2 * QN + c] + sR[3 * QN + c]);
                 s.pre_ml[piece * 2 * QT + c] = M;
                 s.pre_ml[piece * 2 * QT + QT + c] = M == -INFINITY && !isnan(L) ? 0.f : L;
             }
-            if (ht == 0)
-                s.pre_flag[2 * piece + half] = (failed ? PIECE_GAVE_UP : 0) | (*(volatile int *)s_bad ? PIECE_BAD_PAGE : 0);
-            half_bar(half);
+            if (gt == 0)
+                s.pre_flag[4 * piece + grp] = (failed ? PIECE_GAVE_UP : 0) | (*(volatile int *)s_bad ? PIECE_BAD_PAGE : 0);
+            group_bar(grp);
         }
     }
     fence_before_sync();
@@ -519,7 +516,7 @@ cudaError_t run(const PagedStep &a, const PagedPlan &p, const PagedScratch &s, c
     auto k = prefix_tc_kernel<D, QN>;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
-    k<<<p.pre_blocks, NT, C::SMEM, st>>>(mQ, mK, mV, a, s, p);
+    k<<<p.pre_blocks, C::NT, C::SMEM, st>>>(mQ, mK, mV, a, s, p);
     count_launches();
     return cudaGetLastError();
 }

@@ -170,6 +170,7 @@ __global__ void __launch_bounds__(NT, 1) decode_own_kernel(PagedStep a, PagedScr
     const PagedCache &c = a.c;
     const int page = 1 << c.page_log2;
 
+    release_next();
     if (lane == 0) {
         for (int i = 0; i < S; ++i) tc::mbar_init(&s_bar[warp][i], 1);
         tc::mbar_fence_init();
@@ -483,6 +484,8 @@ __global__ void __launch_bounds__(NT, 1) decode_own_kernel(PagedStep a, PagedScr
             for (int i = 0; i < S; ++i)
                 tc::mbar_wait(&s_bar[warp][(st + i) % S], st + i < S ? parity : parity ^ 1, tc::WAIT_LIMIT_NS);
     }
+    // this kernel needs nothing of the ones before it in the call, but completes after them
+    if (SHARED && tid == 0) wait_previous();
     __syncthreads();
 
     // The pieces of the block's warps, in order: neighbours of one unit are put together.
@@ -538,13 +541,24 @@ __global__ void __launch_bounds__(D) decode_join_kernel(PagedStep a, PagedScratc
 {
     const int u = blockIdx.x, b = u / a.H, h = u % a.H, e = threadIdx.x;
     const int slot = slot_of(a.c, b);
-    if (slot < 0) return;  // idle: out stays as it was
-    T *out = static_cast<T *>(a.out) + (long long)u * D + e;
-    bool bad = length_of(a.c, slot) < 0;
-    if (a.c.rows) {  // two batch rows on one slot would update its keys twice
+    bool bad = slot >= 0 && length_of(a.c, slot) < 0;
+    if (a.c.rows && slot >= 0) {  // two batch rows on one slot would update its keys twice
         for (int i = e; i < a.B; i += D) bad |= i != b && a.c.rows[i] == slot;
     }
+    int j0 = 0, j1 = -1, row = 0;
+    long long pu = 0;
+    if (SHARED) {
+        // blocks of the prefix's units: block i holds tiles [total i / n, total (i + 1) / n)
+        pu = (long long)h * p.q_tiles + b / p.q_tile;
+        row = b % p.q_tile;
+        const long long total = (long long)p.pre_units * p.key_tiles, t0 = pu * p.key_tiles;
+        j0 = (int)(((t0 + 1) * p.pre_blocks - 1) / total);
+        j1 = (int)(((t0 + p.key_tiles) * p.pre_blocks - 1) / total);
+    }
+    wait_previous();
     bad = __syncthreads_or(bad);
+    if (slot < 0) return;  // idle: out stays as it was
+    T *out = static_cast<T *>(a.out) + (long long)u * D + e;
     if (bad) {
         *out = from_f<T>(__int_as_float(0x7fc00000));
         if (e == 0) atomicMax(s.err, ERR_PAGE);
@@ -552,24 +566,18 @@ __global__ void __launch_bounds__(D) decode_join_kernel(PagedStep a, PagedScratc
     }
     const int i0 = s.first[u], i1 = s.last[u];
     int flag = 0;
+    float M = -INFINITY;
     for (int i = i0; i <= i1; ++i) flag |= s.own_flag[(long long)i + u];
-    int j0 = 0, j1 = -1, row = 0;
-    long long pu = 0;
-    if (SHARED && a.prefix_len > 0) {
-        // blocks of the prefix's units: block i holds tiles [total i / n, total (i + 1) / n)
-        pu = (long long)h * p.q_tiles + b / p.q_tile;
-        row = b % p.q_tile;
-        const long long total = (long long)p.pre_units * p.key_tiles, t0 = pu * p.key_tiles;
-        j0 = (int)(((t0 + 1) * p.pre_blocks - 1) / total);
-        j1 = (int)(((t0 + p.key_tiles) * p.pre_blocks - 1) / total);
-        for (int j = j0; j <= j1; ++j) flag |= s.pre_flag[4 * (j + pu) + row / 16];
+    if (SHARED || i0 != i1) {  // else the block that held the whole unit wrote out
+        for (int i = i0; i <= i1; ++i) M = fmaxf(M, s.own[((long long)i + u) * (D + 2)]);
+        for (int j = j0; j <= j1; ++j) {
+            flag |= s.pre_flag[4 * (j + pu) + row / 16];
+            M = fmaxf(M, s.pre_ml[(j + pu) * 2 * p.q_tile + row]);
+        }
     }
     flag &= BAD_PAGE | GAVE_UP;
     if (flag && e == 0) atomicMax(s.err, flag & BAD_PAGE ? ERR_PAGE : ERR_PAGED_WAIT);
-    if (!SHARED && i0 == i1) return;  // one block held the whole unit and wrote out
-    float M = -INFINITY;
-    for (int i = i0; i <= i1; ++i) M = fmaxf(M, s.own[((long long)i + u) * (D + 2)]);
-    for (int j = j0; j <= j1; ++j) M = fmaxf(M, s.pre_ml[(j + pu) * 2 * p.q_tile + row]);
+    if (!SHARED && i0 == i1) return;
     float L = 0.f, A = 0.f;
     for (int i = i0; i <= i1; ++i) {
         const float *x = s.own + ((long long)i + u) * (D + 2);
@@ -596,15 +604,17 @@ cudaError_t run(const PagedStep &a, const PagedPlan &p, const PagedScratch &s, c
         constexpr int smem = OwnCfg<T, D>::SMEM;
         cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
-        k<<<p.own_blocks, NT, smem, st>>>(a, s);
-        count_launches();
-        e = cudaGetLastError();
+        if (SHARED) {
+            e = launch_overlapped(k, p.own_blocks, NT, smem, st, a, s);
+        } else {
+            k<<<p.own_blocks, NT, smem, st>>>(a, s);
+            count_launches();
+            e = cudaGetLastError();
+        }
         if (e != cudaSuccess) return e;
     }
     Stage stage("decode_join", st);
-    decode_join_kernel<T, D, SHARED><<<a.B * a.H, D, 0, st>>>(a, s, p);
-    count_launches();
-    return cudaGetLastError();
+    return launch_overlapped(decode_join_kernel<T, D, SHARED>, a.B * a.H, D, 0, st, a, s, p);
 }
 
 template <typename T, int D>

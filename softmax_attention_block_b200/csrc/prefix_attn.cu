@@ -21,17 +21,21 @@ constexpr int NT = 256;
 constexpr float LOG2E = 1.4426950408889634f;
 
 // One (batch row, head): G read once and written once, bound by HBM (8 d^2
-// bytes). A thread keeps D * D / 1024 vectors of four columns in registers.
+// bytes). A thread keeps D * D / 512 vectors of four columns in registers, so that a
+// block's whole G is on its way at once, and only four partial sums of a column meet.
+constexpr int TT = 128;
+
 template <typename T, int D>
-__global__ void __launch_bounds__(NT) turn_kernel(PagedStep a, PagedScratch s, int q_rows)
+__global__ void __launch_bounds__(TT) turn_kernel(PagedStep a, PagedScratch s, int q_rows)
 {
     constexpr int CG = D / 4;       // groups of four columns
-    constexpr int RG = NT / CG;     // rows of a pass
+    constexpr int RG = TT / CG;     // rows of a pass
     constexpr int R = D / RG;       // rows a thread keeps
     __shared__ float sw[D], sq[D];
-    __shared__ float4 red[2][RG][CG];
+    __shared__ float4 red[2][4][CG];
     const int u = blockIdx.x, b = u / a.H, h = u % a.H, tid = threadIdx.x;
-    const int cg = tid % CG, rg = tid / CG;
+    const int cg = tid % CG, rg = tid / CG, warp = tid / 32, lane = tid % 32;
+    release_next();
     const int slot = b < a.B ? slot_of(a.c, b) : -1;
     const long long row = (long long)h * q_rows + b;
     float4 *qt = reinterpret_cast<float4 *>(s.qt) + row * CG;  // fp32
@@ -47,17 +51,21 @@ __global__ void __launch_bounds__(NT) turn_kernel(PagedStep a, PagedScratch s, i
         if (tid == 0) s.qg[row] = 0.f;
         return;
     }
-    if (tid < D) {
-        sw[tid] = to_f(static_cast<const T *>(a.w)[(long long)u * D + tid]);
-        sq[tid] = to_f(static_cast<const T *>(a.q)[(long long)u * D + tid]);
-    }
     float4 *G = reinterpret_cast<float4 *>(a.state) + ((long long)slot * a.H + h) * (D * CG);
     float4 x[R];
 #pragma unroll
     for (int i = 0; i < R; ++i) x[i] = G[(i * RG + rg) * CG + cg];
+    for (int i = tid; i < D; i += TT) {
+        sw[i] = to_f(static_cast<const T *>(a.w)[(long long)u * D + i]);
+        sq[i] = to_f(static_cast<const T *>(a.q)[(long long)u * D + i]);
+    }
+    const float beta = a.beta[u];
     __syncthreads();
-    float4 y = make_float4(0.f, 0.f, 0.f, 0.f), z = y;
     float qw = 0.f;
+#pragma unroll
+    for (int i = lane; i < D; i += 32) qw = fmaf(sq[i], sw[i], qw);
+    qw = group_sum<32>(qw);
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f), z = y;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
         const float w = sw[i * RG + rg], q = sq[i * RG + rg];
@@ -70,20 +78,25 @@ __global__ void __launch_bounds__(NT) turn_kernel(PagedStep a, PagedScratch s, i
         z.z = fmaf(q, x[i].z, z.z);
         z.w = fmaf(q, x[i].w, z.w);
     }
-    red[0][rg][cg] = y;
-    red[1][rg][cg] = z;
-    for (int i = 0; i < D; ++i) qw = fmaf(sq[i], sw[i], qw);
+    if (CG == 16) {  // two rows of a pass in one warp
+        float *f[2] = {&y.x, &z.x};
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[i][e] += __shfl_xor_sync(0xffffffffu, f[i][e], 16);
+    }
+    red[0][warp][cg] = y;
+    red[1][warp][cg] = z;
     __syncthreads();
     y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < RG; ++i) {
+    for (int i = 0; i < 4; ++i) {
         const float4 t = red[0][i][cg];
         y.x += t.x;
         y.y += t.y;
         y.z += t.z;
         y.w += t.w;
     }
-    const float beta = a.beta[u];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
         const float f = -beta * sw[i * RG + rg];
@@ -96,7 +109,7 @@ __global__ void __launch_bounds__(NT) turn_kernel(PagedStep a, PagedScratch s, i
     if (rg == 0) {
         z = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < RG; ++i) {
+        for (int i = 0; i < 4; ++i) {
             const float4 t = red[1][i][cg];
             z.x += t.x;
             z.y += t.y;
@@ -173,6 +186,8 @@ __global__ void __launch_bounds__(NT) prefix_simt_kernel(PagedStep a, PagedScrat
     extern __shared__ float sm[];
     float *sQ = sm + C::Q, *sK = sm + C::K, *sV = sm + C::V, *sP = sm + C::P, *sG = sm + C::G;
     const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
+    release_next();
+    wait_previous();
     const int q_rows = p.q_tiles * QT;
     const float scale2 = a.scale * LOG2E;
     const long long total = (long long)p.pre_units * p.key_tiles;
@@ -300,16 +315,14 @@ cudaError_t run_simt(const PagedStep &a, const PagedPlan &p, const PagedScratch 
     auto k = prefix_simt_kernel<D>;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SimtCfg<D>::SMEM);
     if (e != cudaSuccess) return e;
-    k<<<p.pre_blocks, NT, SimtCfg<D>::SMEM, st>>>(a, s, p);
-    count_launches();
-    return cudaGetLastError();
+    return launch_overlapped(k, p.pre_blocks, NT, SimtCfg<D>::SMEM, st, a, s, p);
 }
 
 template <typename T, int D>
 cudaError_t run_turn(const PagedStep &a, const PagedPlan &p, const PagedScratch &s, cudaStream_t st)
 {
     const int q_rows = p.q_tiles * p.q_tile;
-    turn_kernel<T, D><<<q_rows * a.H, NT, 0, st>>>(a, s, q_rows);
+    turn_kernel<T, D><<<q_rows * a.H, TT, 0, st>>>(a, s, q_rows);
     count_launches();
     return cudaGetLastError();
 }

@@ -131,6 +131,7 @@ __global__ void __launch_bounds__(Cfg<D, QN>::NT, 1)
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const bool gate = a.c.g != nullptr;
 
+    release_next();
     if (tid == 0) {
         for (int i = 0; i < NK; ++i) {
             mbar_init(&k_full[i], 1);
@@ -179,6 +180,7 @@ __global__ void __launch_bounds__(Cfg<D, QN>::NT, 1)
                     ok = false;
                     break;
                 }
+                if (seg == 0) wait_previous();  // the queries; keys and values are nobody's output
                 if (lane == 0) {
                     mbar_expect_tx(q_full, 2 * QT * D * 2);
                     const int row = h * q_rows + (u % p.q_tiles) * QT;
@@ -460,6 +462,7 @@ __global__ void __launch_bounds__(Cfg<D, QN>::NT, 1)
                 }
             }
             // the piece of this unit
+            wait_previous();  // qg
             if (ok && !product_done(n - 1)) ok = false;
             ok = __all_sync(0xffffffffu, ok);
             fence_after_sync();
@@ -516,9 +519,7 @@ cudaError_t run(const PagedStep &a, const PagedPlan &p, const PagedScratch &s, c
     auto k = prefix_tc_kernel<D, QN>;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
-    k<<<p.pre_blocks, C::NT, C::SMEM, st>>>(mQ, mK, mV, a, s, p);
-    count_launches();
-    return cudaGetLastError();
+    return launch_overlapped(k, p.pre_blocks, C::NT, C::SMEM, st, mQ, mK, mV, a, s, p);
 }
 
 }  // namespace

@@ -25,7 +25,8 @@
 // Warps: groups of four for the softmax of 16 queries each (they share nothing but the
 // barriers towards the MMAs; the chain of one group, not its instructions, is what a tile
 // waits for, and 16 columns a thread leave room for three or four groups), then one for the
-// loads (a box of min(page, 128) rows a page, TMA) and one for the MMAs.
+// loads (a box of min(page, 128) rows a page, TMA) and one to issue each of the two products:
+// a single warp takes longer to issue a tile's MMAs than the tensor cores to do them.
 // Waits are bounded; one that gives up makes its pieces NaN and is reported.
 #include "paged.cuh"
 #include "rowvec.cuh"
@@ -47,7 +48,7 @@ constexpr float SLACK = 8.f;
 template <int D, int QN>
 struct Cfg {
     static constexpr int PANELS = D / 64;
-    static constexpr int GROUPS = QN / CN, W_LOAD = 4 * GROUPS, W_MMA = W_LOAD + 1, NT = 32 * (W_MMA + 1);
+    static constexpr int GROUPS = QN / CN, W_LOAD = 4 * GROUPS, W_S = W_LOAD + 1, W_O = W_S + 1, NT = 32 * (W_O + 1);
     static constexpr int TILE = KT * D * 2;             // one operand tile
     static constexpr int NK = D == 64 ? 4 : QN == 32 ? 3 : 2, NV = D == 64 ? 4 : 2, NG = NV + 1;
     static constexpr int Q = 2 * QN * D * 2;            // hi and lo
@@ -116,7 +117,7 @@ __global__ void __launch_bounds__(Cfg<D, QN>::NT, 1)
 {
     using C = Cfg<D, QN>;
     constexpr int NK = C::NK, NV = C::NV, NG = C::NG, NP = C::NP, PANELS = C::PANELS;
-    constexpr int W_LOAD = C::W_LOAD, W_MMA = C::W_MMA;
+    constexpr int W_LOAD = C::W_LOAD, W_S = C::W_S, W_O = C::W_O;
     extern __shared__ uint8_t smraw[];
     uint8_t *sm = smraw + (1024 - (smem_u32(smraw) & 1023)) % 1024;
     uint64_t *k_full = reinterpret_cast<uint64_t *>(sm + C::BAR_OFF), *k_empty = k_full + NK;
@@ -150,11 +151,11 @@ __global__ void __launch_bounds__(Cfg<D, QN>::NT, 1)
             mbar_init(&p_full[i], p.q_tile / CN * 4);  // a warp each
             mbar_init(&o_done[i], 1);
         }
-        mbar_init(mma_done, 1);
+        mbar_init(mma_done, 2);
         mbar_fence_init();
         *s_bad = 0;
     }
-    if (warp == W_MMA) tmem_alloc(tmem_slot, C::TMEM);
+    if (warp == W_O) tmem_alloc(tmem_slot, C::TMEM);
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
@@ -171,10 +172,17 @@ __global__ void __launch_bounds__(Cfg<D, QN>::NT, 1)
         const int npre = (a.prefix_len + page - 1) >> log2p;
         int tab = -1, tab_at = 0, tab_end = 0, issued_k = 0, issued_v = 0, seg = 0;
         bool ok = true;
-        for (int n = 0; n < count && ok; ++n) {
-            const long long t = t0 + n;
-            const int u = (int)(t / p.key_tiles), kt = (int)(t % p.key_tiles);
-            const int h = u / p.q_tiles, key0 = kt * KT;
+        // position in the list, kept by hand: a division a tile would take longer than its loads
+        int u = (int)(t0 / p.key_tiles), kt = (int)(t0 % p.key_tiles), h = u / p.q_tiles, qt = u % p.q_tiles;
+        for (int n = 0; n < count && ok; ++n, ++kt) {
+            if (kt == p.key_tiles) {
+                kt = 0;
+                if (++qt == p.q_tiles) {
+                    qt = 0;
+                    ++h;
+                }
+            }
+            const int key0 = kt * KT;
             if (n == 0 || kt == 0) {
                 if (seg > 0 && !mbar_wait(q_empty, (seg - 1) & 1, WAIT_LIMIT_NS)) {
                     ok = false;
@@ -183,7 +191,7 @@ __global__ void __launch_bounds__(Cfg<D, QN>::NT, 1)
                 if (seg == 0) wait_previous();  // the queries; keys and values are nobody's output
                 if (lane == 0) {
                     mbar_expect_tx(q_full, 2 * QT * D * 2);
-                    const int row = h * q_rows + (u % p.q_tiles) * QT;
+                    const int row = h * q_rows + qt * QT;
                     for (int x = 0; x < PANELS; ++x) {
                         tma_load_2d(sm + C::Q_OFF + x * QN * 128, &mQ, 64 * x, row, q_full);
                         tma_load_2d(sm + C::Q_OFF + (PANELS + x) * QN * 128, &mQ, 64 * x, a.H * q_rows + row, q_full);
@@ -204,7 +212,7 @@ __global__ void __launch_bounds__(Cfg<D, QN>::NT, 1)
             if (in && !good) *s_bad = 1;
             const int cnt = __popc(__ballot_sync(0xffffffffu, good));
             const int row = good ? (int)((((long long)pid * a.H + h) << log2p) + (key & (page - 1))) : 0;
-            const int ks = n % NK, vs = n % NV, gs = n % NG;
+            const uint32_t ks = (uint32_t)n % NK, vs = (uint32_t)n % NV, gs = (uint32_t)n % NG;
             if (n >= NK && !mbar_wait(&k_empty[ks], (n / NK - 1) & 1, WAIT_LIMIT_NS)) ok = false;
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
@@ -247,58 +255,61 @@ __global__ void __launch_bounds__(Cfg<D, QN>::NT, 1)
                 mbar_wait(&v_full[n % NV], (n / NV) & 1, WAIT_LIMIT_NS);
             if (seg > 0) mbar_wait(q_full, (seg - 1) & 1, WAIT_LIMIT_NS);
         }
-    } else if (warp == W_MMA) {
-        // The whole warp runs along, converged, and one lane issues: descriptors stay uniform.
-        // A product of 16 keys or dims takes about 72 cycles whatever its other sides are: a tile
-        // has D / 8 of S^T (hi and lo one after the other) and 8 of O^T (hi | lo as columns), 1150 at
-        // D = 64 and 1700 at 128, where its loads take 1400 and 2800.
+    } else if (warp == W_S) {
+        // S^T = K . qt^T, hi then lo. The whole warp runs along, converged, and one lane issues:
+        // descriptors stay uniform, and differ from a base by the address in their low bits.
         const uint32_t issue = lane == 0;
-        const uint32_t idS = idesc_f16(128, QT, AB_BF16, 0, 0), idO = idesc_f16(D, QN + QT, AB_BF16, 1, 1);
-        const uint32_t q_addr = smem_u32(sm + C::Q_OFF), p_addr = smem_u32(sm + C::P_OFF);
-        int kt = (int)(t0 % p.key_tiles), seg = 0;  // of the S product issued next
-        auto issue_s = [&](int n) -> bool {
-            const int ks = n % NK;
-            bool ok = true;
+        const uint32_t id = idesc_f16(128, QT, AB_BF16, 0, 0);
+        const uint64_t k0 = desc_sw128(smem_u32(sm + C::K_OFF), 16, 1024), q0 = desc_sw128(smem_u32(sm + C::Q_OFF), 16, 1024);
+        int kt = (int)(t0 % p.key_tiles), seg = 0;
+        bool ok = true;
+        for (int n = 0; n < count; ++n) {
+            const uint32_t ks = (uint32_t)n % NK;
             if (n == 0 || kt == 0) ok = mbar_wait(q_full, seg++ & 1, WAIT_LIMIT_NS);
             ok = ok && mbar_wait(&k_full[ks], (n / NK) & 1, WAIT_LIMIT_NS);
-            if (!__all_sync(0xffffffffu, ok)) return false;
+            // the buffer of S^T was read before the weights of tile n - 2 were complete
+            if (n >= 2) ok = ok && mbar_wait(&p_full[n & 1], ((n >> 1) - 1) & 1, WAIT_LIMIT_NS);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
             fence_after_sync();
-            const uint32_t k_addr = smem_u32(sm + C::K_OFF + ks * C::TILE);
+            const uint64_t kd = k0 + ks * (C::TILE >> 4);
+            const uint32_t d = tbase + C::T_S + (n & 1) * QN;
 #pragma unroll
             for (int part = 0; part < 2; ++part)
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
-                    mma_ss_if(issue, tbase + C::T_S + (n & 1) * QN,
-                              desc_sw128(k_addr + (kk / 4) * KT * 128 + (kk % 4) * 32, 16, 1024),
-                              desc_sw128(q_addr + (part * PANELS + kk / 4) * QN * 128 + (kk % 4) * 32, 16, 1024),
-                              idS, part + kk > 0);
+                    mma_ss_if(issue, d, kd + (((kk / 4) * KT * 128 + (kk % 4) * 32) >> 4),
+                              q0 + (((part * PANELS + kk / 4) * QN * 128 + (kk % 4) * 32) >> 4), id, part + kk > 0);
             commit_if(issue, &s_full[n & 1]);
             commit_if(issue, &k_empty[ks]);
             if (++kt == p.key_tiles) kt = 0;
             if (n + 1 == count || kt == 0) commit_if(issue, q_empty);
-            return true;
-        };
-        bool ok = count > 0 && issue_s(0);
-        int kv = (int)(t0 % p.key_tiles);
-        for (int n = 0; ok && n < count; ++n) {
-            // the buffer of S(n + 1) was read before P(n - 1) was complete
-            if (n + 1 < count && !issue_s(n + 1)) break;
-            const int vs = n % NV;
+        }
+        // the tensor memory is freed after the issuing warps leave: no MMA may still be running then
+        commit_if(issue, mma_done);
+        mbar_wait(mma_done, 0, 8 * WAIT_LIMIT_NS);
+    } else if (warp == W_O) {
+        // O^T += V^T . P, hi | lo as columns
+        const uint32_t issue = lane == 0;
+        const uint32_t id = idesc_f16(D, QN + QT, AB_BF16, 1, 1);
+        const uint64_t v0 = desc_sw128(smem_u32(sm + C::V_OFF), KT * 128, 1024), p0 = desc_sw128(smem_u32(sm + C::P_OFF), C::PP, 1024);
+        int kt = (int)(t0 % p.key_tiles);
+        bool ok = true;
+        for (int n = 0; n < count; ++n) {
+            const uint32_t vs = (uint32_t)n % NV;
             ok = mbar_wait(&v_full[vs], (n / NV) & 1, WAIT_LIMIT_NS) && mbar_wait(&p_full[n & 1], (n >> 1) & 1, WAIT_LIMIT_NS);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             fence_after_sync();
-            const uint32_t v_addr = smem_u32(sm + C::V_OFF + vs * C::TILE);
-            const bool fresh = n == 0 || kv == 0;
-            if (++kv == p.key_tiles) kv = 0;
+            const uint64_t vd = v0 + vs * (C::TILE >> 4), pd = p0 + (n % NP) * (C::P >> 4);
+            const bool fresh = n == 0 || kt == 0;
+            if (++kt == p.key_tiles) kt = 0;
 #pragma unroll
             for (int kk = 0; kk < KT / 16; ++kk)
-                mma_ss_if(issue, tbase + C::T_O, desc_sw128(v_addr + kk * 2048, KT * 128, 1024),
-                          desc_sw128(p_addr + (n % NP) * C::P + kk * 2048, C::PP, 1024), idO, !fresh || kk > 0);
+                mma_ss_if(issue, tbase + C::T_O, vd + (kk * 2048 >> 4), pd + (kk * 2048 >> 4), id, !fresh || kk > 0);
             commit_if(issue, &v_empty[vs]);
             commit_if(issue, &o_done[n & 1]);
         }
-        // the tensor memory is freed after this warp leaves: no MMA may still be running then
         commit_if(issue, mma_done);
         mbar_wait(mma_done, 0, 8 * WAIT_LIMIT_NS);
     } else if (warp / 4 * CN < QT) {
@@ -502,7 +513,7 @@ __global__ void __launch_bounds__(Cfg<D, QN>::NT, 1)
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
-    if (warp == W_MMA) tmem_dealloc(tbase, C::TMEM);
+    if (warp == W_O) tmem_dealloc(tbase, C::TMEM);
 }
 
 template <int D, int QN>

@@ -45,10 +45,11 @@ constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LOW = -1e30f;  // reference of a query that has no weight yet
 constexpr float SLACK = 8.f;
 
-template <int D, int QN>
+// GROUPS softmax groups: units of QT = 16 GROUPS queries. QN is the room for them.
+template <int D, int GROUPS>
 struct Cfg {
-    static constexpr int PANELS = D / 64;
-    static constexpr int GROUPS = QN / CN, W_LOAD = 4 * GROUPS, W_S = W_LOAD + 1, W_O = W_S + 1, NT = 32 * (W_O + 1);
+    static constexpr int PANELS = D / 64, QT = CN * GROUPS, QN = QT <= 32 ? 32 : 64;
+    static constexpr int W_LOAD = 4 * GROUPS, W_S = W_LOAD + 1, W_O = W_S + 1, NT = 32 * (W_O + 1);
     static constexpr int TILE = KT * D * 2;             // one operand tile
     static constexpr int NK = D == 64 ? 4 : QN == 32 ? 3 : 2, NV = D == 64 ? 4 : 2, NG = NV + 1;
     static constexpr int Q = 2 * QN * D * 2;            // hi and lo
@@ -58,7 +59,7 @@ struct Cfg {
     static constexpr int K_OFF = 0, V_OFF = K_OFF + NK * TILE, Q_OFF = V_OFF + NV * TILE, P_OFF = Q_OFF + Q;
     static constexpr int G_OFF = P_OFF + NP * P, M_OFF = G_OFF + NG * KT * 4, F_OFF = M_OFF + QN * 4;
     static constexpr int RED_OFF = F_OFF + QN * 4, BAR_OFF = RED_OFF + 4 * QN * 4;
-    static constexpr int NBAR = 2 * NK + 2 * NV + NG + 9;
+    static constexpr int NBAR = 2 * NK + 2 * NV + NG + 11;
     static constexpr int SMEM = BAR_OFF + NBAR * 8 + 16 + 1024;
     static constexpr int T_S = 0, T_O = 2 * QN, TMEM = 4 * QN;  // two S^T, then O^T for hi | lo
     static_assert(SMEM <= 232448, "shared memory");
@@ -110,12 +111,13 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-template <int D, int QN>
-__global__ void __launch_bounds__(Cfg<D, QN>::NT, 1)
+template <int D, int GROUPS>
+__global__ void __launch_bounds__(Cfg<D, GROUPS>::NT, 1)
     prefix_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
                      const __grid_constant__ CUtensorMap mV, PagedStep a, PagedScratch s, PagedPlan p)
 {
-    using C = Cfg<D, QN>;
+    using C = Cfg<D, GROUPS>;
+    constexpr int QT = C::QT, QN = C::QN;
     constexpr int NK = C::NK, NV = C::NV, NG = C::NG, NP = C::NP, PANELS = C::PANELS;
     constexpr int W_LOAD = C::W_LOAD, W_S = C::W_S, W_O = C::W_O;
     extern __shared__ uint8_t smraw[];
@@ -124,8 +126,8 @@ __global__ void __launch_bounds__(Cfg<D, QN>::NT, 1)
     uint64_t *v_full = k_empty + NK, *v_empty = v_full + NV, *g_full = v_empty + NV;
     uint64_t *q_full = g_full + NG, *q_empty = q_full + 1, *s_full = q_full + 2, *p_full = q_full + 4;
     // P and its product: a barrier for each parity of the tile, since one group may be a tile ahead
-    uint64_t *o_done = q_full + 6, *mma_done = q_full + 8;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(q_full + 9);
+    uint64_t *o_done = q_full + 6, *mma_done = q_full + 8, *s_empty = q_full + 9;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(q_full + 11);
     int *s_bad = reinterpret_cast<int *>(tmem_slot + 1);
     float *sG = reinterpret_cast<float *>(sm + C::G_OFF), *sM = reinterpret_cast<float *>(sm + C::M_OFF);
     float *sF = reinterpret_cast<float *>(sm + C::F_OFF), *sR = reinterpret_cast<float *>(sm + C::RED_OFF);
@@ -148,7 +150,8 @@ __global__ void __launch_bounds__(Cfg<D, QN>::NT, 1)
         mbar_init(&s_full[0], 1);
         mbar_init(&s_full[1], 1);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&p_full[i], p.q_tile / CN * 4);  // a warp each
+            mbar_init(&p_full[i], 4 * GROUPS);  // a warp each
+            mbar_init(&s_empty[i], 4 * GROUPS);
             mbar_init(&o_done[i], 1);
         }
         mbar_init(mma_done, 2);
@@ -165,7 +168,7 @@ __global__ void __launch_bounds__(Cfg<D, QN>::NT, 1)
     const long long total = (long long)p.pre_units * p.key_tiles;
     const long long t0 = total * blockIdx.x / gridDim.x, t1 = total * (blockIdx.x + 1) / gridDim.x;
     const int count = (int)(t1 - t0);
-    const int QT = p.q_tile, q_rows = p.q_tiles * QT;  // queries of a unit: a multiple of 16, at most QN
+    const int q_rows = p.q_tiles * QT;
 
     if (warp == W_LOAD) {
         const int log2p = a.c.page_log2, page = 1 << log2p, box = page < KT ? page : KT, boxes = KT / box;
@@ -259,7 +262,7 @@ __global__ void __launch_bounds__(Cfg<D, QN>::NT, 1)
         // S^T = K . qt^T, hi then lo. The whole warp runs along, converged, and one lane issues:
         // descriptors stay uniform, and differ from a base by the address in their low bits.
         const uint32_t issue = lane == 0;
-        const uint32_t id = idesc_f16(128, QT, AB_BF16, 0, 0);
+        constexpr uint32_t id = idesc_f16(128, QT, AB_BF16, 0, 0);
         const uint64_t k0 = desc_sw128(smem_u32(sm + C::K_OFF), 16, 1024), q0 = desc_sw128(smem_u32(sm + C::Q_OFF), 16, 1024);
         int kt = (int)(t0 % p.key_tiles), seg = 0;
         bool ok = true;
@@ -267,8 +270,7 @@ __global__ void __launch_bounds__(Cfg<D, QN>::NT, 1)
             const uint32_t ks = (uint32_t)n % NK;
             if (n == 0 || kt == 0) ok = mbar_wait(q_full, seg++ & 1, WAIT_LIMIT_NS);
             ok = ok && mbar_wait(&k_full[ks], (n / NK) & 1, WAIT_LIMIT_NS);
-            // the buffer of S^T was read before the weights of tile n - 2 were complete
-            if (n >= 2) ok = ok && mbar_wait(&p_full[n & 1], ((n >> 1) - 1) & 1, WAIT_LIMIT_NS);
+            if (n >= 2) ok = ok && mbar_wait(&s_empty[n & 1], ((n >> 1) - 1) & 1, WAIT_LIMIT_NS);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             fence_after_sync();
@@ -291,7 +293,7 @@ __global__ void __launch_bounds__(Cfg<D, QN>::NT, 1)
     } else if (warp == W_O) {
         // O^T += V^T . P, hi | lo as columns
         const uint32_t issue = lane == 0;
-        const uint32_t id = idesc_f16(D, QN + QT, AB_BF16, 1, 1);
+        constexpr uint32_t id = idesc_f16(D, QN + QT, AB_BF16, 1, 1);
         const uint64_t v0 = desc_sw128(smem_u32(sm + C::V_OFF), KT * 128, 1024), p0 = desc_sw128(smem_u32(sm + C::P_OFF), C::PP, 1024);
         int kt = (int)(t0 % p.key_tiles);
         bool ok = true;
@@ -312,15 +314,24 @@ __global__ void __launch_bounds__(Cfg<D, QN>::NT, 1)
         }
         commit_if(issue, mma_done);
         mbar_wait(mma_done, 0, 8 * WAIT_LIMIT_NS);
-    } else if (warp / 4 * CN < QT) {
+    } else {
         // thread = key of the tile (a lane of S^T), queries c0 .. c0 + 15; then a row of O^T: dim gt,
-        // or at D = 64 dim 16 (warp % 4) + lane in the lanes below 16
+        // or at D = 64 dim 16 (warp % 4) + lane in the lanes below 16. Waits that give up leave a mark
+        // and go on (every address is fixed, every barrier is still met): the pieces become NaN.
         const int grp = warp / 4, gt = tid % 128, c0 = grp * CN;
         const uint32_t lane_off = (uint32_t)(32 * (warp % 4)) << 16;
-        const F2 scale2 = f2(a.scale * LOG2E, a.scale * LOG2E);
-        bool ok = true;
+        const F2 scale2 = f2(a.scale * LOG2E, a.scale * LOG2E), minus1 = f2(-1.f, -1.f);
+        bool gave_up = false;
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            if (!mbar_try_wait(bar, parity) && !gave_up) gave_up = !mbar_wait(bar, parity, WAIT_LIMIT_NS);
+            __syncwarp();
+        };
+        auto product_done = [&](int i) { wait(&o_done[i & 1], (i >> 1) & 1); };
+        // this thread's row of P: chunk j of eight queries, hi and lo
+        const uint32_t hi0 = sw128_offset(gt, c0), hi1 = sw128_offset(gt, c0 + 8);
+        const uint32_t lo0 = QN == 32 ? sw128_offset(gt, 32 + c0) : C::PP + hi0, lo1 = QN == 32 ? sw128_offset(gt, 40 + c0) : C::PP + hi1;
+        uint32_t gslot = 0, gparity = 0;
         int n = 0;
-        auto product_done = [&](int i) { return mbar_wait(&o_done[i & 1], (i >> 1) & 1, WAIT_LIMIT_NS); };
         while (n < count) {
             const long long t = t0 + n;
             const int u = (int)(t / p.key_tiles), kb = (int)(t % p.key_tiles);
@@ -333,26 +344,20 @@ __global__ void __launch_bounds__(Cfg<D, QN>::NT, 1)
             for (int kt = kb; kt < ke; ++kt, ++n) {
                 const bool first = kt == kb, tail = (kt + 1) * KT > a.prefix_len;
                 const bool live = !tail || kt * KT + gt < a.prefix_len;
-                if (ok && !mbar_wait(&s_full[n & 1], (n >> 1) & 1, WAIT_LIMIT_NS)) ok = false;
-                float g = 0.f;
-                if (gate) {
-                    if (ok && !mbar_wait(&g_full[n % NG], (n / NG) & 1, WAIT_LIMIT_NS)) ok = false;
-                    if (ok) g = sG[(n % NG) * KT + gt] * LOG2E;
-                }
-                ok = __all_sync(0xffffffffu, ok);
+                float v[CN], g = 0.f;
+                wait(&s_full[n & 1], (n >> 1) & 1);
                 fence_after_sync();
-                F2 z[CN / 2];
-                const F2 g2 = f2(g, g);
-                auto logits = [&]() {
-                    float v[CN];
-                    tmem_ld16_wait(tbase + C::T_S + (n & 1) * QN + c0 + lane_off, v);
-#pragma unroll
-                    for (int i = 0; i < CN / 2; ++i) z[i] = fma2(f2(v[2 * i], v[2 * i + 1]), scale2, g2);
-                    if (!live) {  // the page's rows behind the prefix hold anything
-#pragma unroll
-                        for (int i = 0; i < CN / 2; ++i) z[i] = f2(-INFINITY, -INFINITY);
+                tmem_ld16(tbase + C::T_S + (n & 1) * QN + c0 + lane_off, v);
+                if (gate) {
+                    wait(&g_full[gslot], gparity);
+                    g = sG[gslot * KT + gt] * LOG2E;
+                    if (++gslot == NG) {
+                        gslot = 0;
+                        gparity ^= 1;
                     }
-                };
+                }
+                const F2 g2 = f2(g, g);
+                F2 z[CN / 2];
                 auto minus_ref = [&]() {
 #pragma unroll
                     for (int i = 0; i < CN / 2; i += 2) {
@@ -361,39 +366,41 @@ __global__ void __launch_bounds__(Cfg<D, QN>::NT, 1)
                         z[i + 1] = add2(z[i + 1], m.y);
                     }
                 };
-                float top = -INFINITY;
-                if (ok && nq > 0) {
-                    logits();
-                    if (!first) {
-                        minus_ref();
+                tmem_wait_ld_tied(v);
+                fence_before_sync();
+                if (lane == 0) mbar_arrive(&s_empty[n & 1]);
+                auto logits = [&]() {
 #pragma unroll
-                        for (int i = 0; i < CN / 2; ++i) {
-                            float x, y;
-                            split(z[i], x, y);
-                            asm("max.f32 %0, %0, %1, %2;" : "+f"(top) : "f"(x), "f"(y));
-                        }
+                    for (int i = 0; i < CN / 2; ++i) z[i] = fma2(f2(v[2 * i], v[2 * i + 1]), scale2, g2);
+                    if (!live) {  // the page's rows behind the prefix hold anything
+#pragma unroll
+                        for (int i = 0; i < CN / 2; ++i) z[i] = f2(-INFINITY, -INFINITY);
+                    }
+                };
+                logits();
+                float top = -INFINITY;
+                if (!first) {
+                    minus_ref();
+#pragma unroll
+                    for (int i = 0; i < CN / 2; ++i) {
+                        float x, y;
+                        split(z[i], x, y);
+                        asm("max.f32 %0, %0, %1, %2;" : "+f"(top) : "f"(x), "f"(y));
                     }
                 }
-                // the buffer of P is free once the product of the tile that had it is done
-                uint8_t *sP = sm + C::P_OFF + (n % NP) * C::P;
-                if (ok && n >= NP && !product_done(n - NP)) ok = false;
-                ok = __all_sync(0xffffffffu, ok);
                 if (group_any(grp, first || top > SLACK)) {
-                    if (ok && nq > 0) {
-                        fence_after_sync();
-                        logits();
-                        float mine = -INFINITY;
+                    logits();
+                    float mine = -INFINITY;
 #pragma unroll
-                        for (int i = 0; i < CN / 2; ++i) {
-                            float x, y;
-                            split(z[i], x, y);
-                            x = warp_max(x);
-                            y = warp_max(y);
-                            if (lane == 2 * i) mine = x;
-                            if (lane == 2 * i + 1) mine = y;
-                        }
-                        if (lane < CN) sR[(warp % 4) * QN + c0 + lane] = mine;
+                    for (int i = 0; i < CN / 2; ++i) {
+                        float x, y;
+                        split(z[i], x, y);
+                        x = warp_max(x);
+                        y = warp_max(y);
+                        if (lane == 2 * i) mine = x;
+                        if (lane == 2 * i + 1) mine = y;
                     }
+                    if (lane < CN) sR[(warp % 4) * QN + c0 + lane] = mine;
                     group_bar(grp);
                     if (gt < CN) {
                         const int c = c0 + gt;
@@ -404,98 +411,87 @@ __global__ void __launch_bounds__(Cfg<D, QN>::NT, 1)
                         sF[c] = ex2(old - x);
                     }
                     group_bar(grp);
-                    if (ok && !first && !product_done(n - 1)) ok = false;
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (ok && nq > 0) {
-                        if (!first) {
-                            fence_after_sync();
+                    if (!first) {
+                        product_done(n - 1);
+                        fence_after_sync();
 #pragma unroll
-                            for (int i = 0; i < CN / 2; ++i)
-                                l[i] = mul2(l[i], f2(sF[c0 + 2 * i], sF[c0 + 2 * i + 1]));
+                        for (int i = 0; i < CN / 2; ++i) l[i] = mul2(l[i], f2(sF[c0 + 2 * i], sF[c0 + 2 * i + 1]));
 #pragma unroll 1
-                            for (int part = 0; part < 2; ++part) {  // hi, lo
-                                const uint32_t at = tbase + C::T_O + part * QN + c0 + lane_off;
-                                float v[CN];
-                                tmem_ld16_wait(at, v);
+                        for (int part = 0; part < 2; ++part) {  // hi, lo
+                            const uint32_t at = tbase + C::T_O + part * QN + c0 + lane_off;
+                            float o[CN];
+                            tmem_ld16_wait(at, o);
 #pragma unroll
-                                for (int i = 0; i < CN; i += 8) {
-                                    uint32_t r[8];
+                            for (int i = 0; i < CN; i += 8) {
+                                uint32_t r[8];
 #pragma unroll
-                                    for (int e = 0; e < 8; ++e) r[e] = __float_as_uint(v[i + e] * sF[c0 + i + e]);
-                                    tmem_st8(at + i, r);
-                                }
+                                for (int e = 0; e < 8; ++e) r[e] = __float_as_uint(o[i + e] * sF[c0 + i + e]);
+                                tmem_st8(at + i, r);
                             }
-                            tmem_wait_st();
                         }
-                        minus_ref();
+                        tmem_wait_st();
+                    }
+                    minus_ref();
+                }
+                // weights, split in two bf16 numbers; this thread's key is a row of P, whose buffer is
+                // free once the product of the tile that had it is done
+                if (n >= NP) product_done(n - NP);
+                uint8_t *sP = sm + C::P_OFF + (n % NP) * C::P;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float x, y;
+                        split(z[4 * j + e], x, y);
+                        x = ex2(x);
+                        y = ex2(y);
+                        const F2 xy = f2(x, y);
+                        l[4 * j + e] = add2(l[4 * j + e], xy);
+                        hi[e] = pack_bf16(x, y);
+                        split(fma2(f2(__uint_as_float(hi[e] << 16), __uint_as_float(hi[e] & 0xffff0000u)), minus1, xy), x, y);
+                        lo[e] = pack_bf16(x, y);
+                    }
+                    *reinterpret_cast<uint4 *>(sP + (j ? hi1 : hi0)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4 *>(sP + (j ? lo1 : lo0)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
+                // values behind the prefix's end are whatever the page holds, and are weighed with
+                // zero: make them zero too
+                if (tail && grp == 0) {
+                    wait(&v_full[n % NV], (n / NV) & 1);
+                    if (!live) {
+                        uint8_t *x = sm + C::V_OFF + (n % NV) * C::TILE + gt * 128;
+#pragma unroll
+                        for (int i = 0; i < PANELS * 8; ++i)
+                            *reinterpret_cast<uint4 *>(x + (i / 8) * KT * 128 + (i % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
                     }
                 }
-                if (ok) {
-                    // weights, split in two bf16 numbers; this thread's key is a row of P
-                    const F2 minus1 = f2(-1.f, -1.f);
-#pragma unroll
-                    for (int i = 0; i < CN; i += 8) {
-                        if (i >= nq) break;
-                        uint32_t hi[4], lo[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            float x, y;
-                            split(z[i / 2 + e], x, y);
-                            x = ex2(x);
-                            y = ex2(y);
-                            const F2 xy = f2(x, y);
-                            l[i / 2 + e] = add2(l[i / 2 + e], xy);
-                            hi[e] = pack_bf16(x, y);
-                            split(fma2(f2(__uint_as_float(hi[e] << 16), __uint_as_float(hi[e] & 0xffff0000u)), minus1, xy), x, y);
-                            lo[e] = pack_bf16(x, y);
-                        }
-                        *reinterpret_cast<uint4 *>(sP + sw128_offset(gt, c0 + i)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                        uint8_t *low = QN == 32 ? sP + sw128_offset(gt, 32 + c0 + i) : sP + C::PP + sw128_offset(gt, c0 + i);
-                        *reinterpret_cast<uint4 *>(low) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                    }
-                    // values behind the prefix's end are whatever the page holds, and are weighed
-                    // with zero: make them zero too
-                    if (tail && grp == 0) {
-                        if (!mbar_wait(&v_full[n % NV], (n / NV) & 1, WAIT_LIMIT_NS)) ok = false;
-                        if (ok && !live) {
-                            uint8_t *v = sm + C::V_OFF + (n % NV) * C::TILE + gt * 128;
-#pragma unroll
-                            for (int x = 0; x < PANELS; ++x)
-#pragma unroll
-                                for (int i = 0; i < 128; i += 16)
-                                    *reinterpret_cast<uint4 *>(v + x * KT * 128 + i) = make_uint4(0u, 0u, 0u, 0u);
-                        }
-                    }
-                    fence_async_smem();
-                    fence_before_sync();
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (ok && lane == 0) mbar_arrive(&p_full[n & 1]);
-                }
+                fence_async_smem();
+                fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[n & 1]);
             }
             // the piece of this unit
             wait_previous();  // qg
-            if (ok && !product_done(n - 1)) ok = false;
-            ok = __all_sync(0xffffffffu, ok);
+            product_done(n - 1);
             fence_after_sync();
             const long long piece = (long long)blockIdx.x + u;
-            if (nq > 0) {
+            {
                 const int dim = D == 128 ? gt : 16 * (warp % 4) + lane;
                 float v[CN], v2[CN];
-                if (ok) {
-                    tmem_ld16_wait(tbase + C::T_O + c0 + lane_off, v);
-                    tmem_ld16_wait(tbase + C::T_O + QN + c0 + lane_off, v2);
-                    if (D == 128 || lane < 16) {
+                tmem_ld16_wait(tbase + C::T_O + c0 + lane_off, v);
+                tmem_ld16_wait(tbase + C::T_O + QN + c0 + lane_off, v2);
+                if (D == 128 || lane < 16) {
 #pragma unroll
-                        for (int i = 0; i < CN; ++i)
-                            if (i < nq) s.pre[(piece * QT + c0 + i) * D + dim] = v[i] + v2[i];
-                    }
+                    for (int i = 0; i < CN; ++i)
+                        if (i < nq) s.pre[(piece * QT + c0 + i) * D + dim] = v[i] + v2[i];
                 }
 #pragma unroll
                 for (int i = 0; i < CN / 2; ++i) split(l[i], v[2 * i], v[2 * i + 1]);
                 const float sum = warp_sums(v);
                 if (lane < CN) sR[(warp % 4) * QN + c0 + lane] = sum;
             }
-            const bool failed = group_any(grp, !ok);
+            const bool failed = group_any(grp, gave_up);
             if (gt < nq) {
                 // the gate since the prefix's end weighs every key of it alike; where it leaves
                 // nothing (log f = -inf), neither the sum nor the values count
@@ -516,10 +512,10 @@ __global__ void __launch_bounds__(Cfg<D, QN>::NT, 1)
     if (warp == W_O) tmem_dealloc(tbase, C::TMEM);
 }
 
-template <int D, int QN>
+template <int D, int GROUPS>
 cudaError_t run(const PagedStep &a, const PagedPlan &p, const PagedScratch &s, cudaStream_t st)
 {
-    using C = Cfg<D, QN>;
+    using C = Cfg<D, GROUPS>;
     const int page = 1 << a.c.page_log2;
     const uint64_t rows = (uint64_t)a.c.n_pages * a.H * page;
     CUtensorMap mQ, mK, mV;
@@ -527,10 +523,21 @@ cudaError_t run(const PagedStep &a, const PagedPlan &p, const PagedScratch &s, c
         !make_map_2d(&mK, a.c.k, BF16, D, rows, page < KT ? page : KT) ||
         !make_map_2d(&mV, a.c.v, BF16, D, rows, page < KT ? page : KT))
         return cudaErrorInvalidValue;
-    auto k = prefix_tc_kernel<D, QN>;
+    auto k = prefix_tc_kernel<D, GROUPS>;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     return launch_overlapped(k, p.pre_blocks, C::NT, C::SMEM, st, mQ, mK, mV, a, s, p);
+}
+
+template <int D>
+cudaError_t run(const PagedStep &a, const PagedPlan &p, const PagedScratch &s, cudaStream_t st)
+{
+    switch (p.q_tile / CN) {
+    case 1: return run<D, 1>(a, p, s, st);
+    case 2: return run<D, 2>(a, p, s, st);
+    case 3: return run<D, 3>(a, p, s, st);
+    default: return run<D, 4>(a, p, s, st);
+    }
 }
 
 }  // namespace
@@ -538,8 +545,7 @@ cudaError_t run(const PagedStep &a, const PagedPlan &p, const PagedScratch &s, c
 cudaError_t prefix_attn_tc(const PagedStep &a, int d, const PagedPlan &p, const PagedScratch &s, cudaStream_t st)
 {
     Stage stage("prefix_attn", st);
-    if (d == 64) return p.q_tile <= 32 ? run<64, 32>(a, p, s, st) : run<64, 64>(a, p, s, st);
-    return p.q_tile <= 32 ? run<128, 32>(a, p, s, st) : run<128, 64>(a, p, s, st);
+    return d == 64 ? run<64>(a, p, s, st) : run<128>(a, p, s, st);
 }
 
 }  // namespace path

@@ -534,18 +534,22 @@ __global__ void __launch_bounds__(NT, 1) decode_own_kernel(PagedStep a, PagedScr
     }
 }
 
-// One (batch row, head): the pieces of its own part in block order, then the
-// prefix's in block order. D threads.
+// One (batch row, head): the pieces of its own part in block order, then the prefix's in block
+// order. Their weights are worked out by the threads side by side, a batch of pieces at a time;
+// then each of the D threads adds up one output element, its loads in flight together.
+constexpr int JOIN_BATCH = 128;
+
 template <typename T, int D, bool SHARED>
 __global__ void __launch_bounds__(D) decode_join_kernel(PagedStep a, PagedScratch s, PagedPlan p)
 {
+    __shared__ float s_f[JOIN_BATCH], s_red[2][D / 32];
     const int u = blockIdx.x, b = u / a.H, h = u % a.H, e = threadIdx.x;
     const int slot = slot_of(a.c, b);
     bool bad = slot >= 0 && length_of(a.c, slot) < 0;
     if (a.c.rows && slot >= 0) {  // two batch rows on one slot would update its keys twice
         for (int i = e; i < a.B; i += D) bad |= i != b && a.c.rows[i] == slot;
     }
-    int j0 = 0, j1 = -1, row = 0;
+    int j0 = 0, nj = 0, row = 0;
     long long pu = 0;
     if (SHARED) {
         // blocks of the prefix's units: block i holds tiles [total i / n, total (i + 1) / n)
@@ -553,7 +557,7 @@ __global__ void __launch_bounds__(D) decode_join_kernel(PagedStep a, PagedScratc
         row = b % p.q_tile;
         const long long total = (long long)p.pre_units * p.key_tiles, t0 = pu * p.key_tiles;
         j0 = (int)(((t0 + 1) * p.pre_blocks - 1) / total);
-        j1 = (int)(((t0 + p.key_tiles) * p.pre_blocks - 1) / total);
+        nj = (int)(((t0 + p.key_tiles) * p.pre_blocks - 1) / total) - j0 + 1;
     }
     wait_previous();
     bad = __syncthreads_or(bad);
@@ -564,34 +568,68 @@ __global__ void __launch_bounds__(D) decode_join_kernel(PagedStep a, PagedScratc
         if (e == 0) atomicMax(s.err, ERR_PAGE);
         return;
     }
-    const int i0 = s.first[u], i1 = s.last[u];
+    const int i0 = s.first[u], ni = s.last[u] - i0 + 1, np = ni + nj;
+    // piece k: its maximum, sum, accumulator and flags
+    auto ml = [&](int k, float &m, float &l, int &flag) {
+        if (k < ni) {
+            const long long x = (long long)i0 + k + u;
+            m = s.own[x * (D + 2)];
+            l = s.own[x * (D + 2) + 1];
+            flag |= s.own_flag[x];
+        } else {
+            const long long x = (long long)j0 + k - ni + pu;
+            m = s.pre_ml[x * 2 * p.q_tile + row];
+            l = s.pre_ml[x * 2 * p.q_tile + p.q_tile + row];
+            flag |= s.pre_flag[4 * x + row / 16];
+        }
+    };
     int flag = 0;
     float M = -INFINITY;
-    for (int i = i0; i <= i1; ++i) flag |= s.own_flag[(long long)i + u];
-    if (SHARED || i0 != i1) {  // else the block that held the whole unit wrote out
-        for (int i = i0; i <= i1; ++i) M = fmaxf(M, s.own[((long long)i + u) * (D + 2)]);
-        for (int j = j0; j <= j1; ++j) {
-            flag |= s.pre_flag[4 * (j + pu) + row / 16];
-            M = fmaxf(M, s.pre_ml[(j + pu) * 2 * p.q_tile + row]);
+    if (!SHARED && ni == 1) {  // the block that held the whole unit wrote out
+        flag = s.own_flag[(long long)i0 + u];
+    } else {
+        for (int k = e; k < np; k += D) {
+            float m, l;
+            ml(k, m, l, flag);
+            M = fmaxf(M, m);
         }
     }
     flag &= BAD_PAGE | GAVE_UP;
-    if (flag && e == 0) atomicMax(s.err, flag & BAD_PAGE ? ERR_PAGE : ERR_PAGED_WAIT);
-    if (!SHARED && i0 == i1) return;
+    if (flag) atomicMax(s.err, flag & BAD_PAGE ? ERR_PAGE : ERR_PAGED_WAIT);
+    if (!SHARED && ni == 1) return;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    if (e % 32 == 0) s_red[0][e / 32] = M;
+    bad = __syncthreads_or(flag);
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) M = fmaxf(M, s_red[0][i]);
     float L = 0.f, A = 0.f;
-    for (int i = i0; i <= i1; ++i) {
-        const float *x = s.own + ((long long)i + u) * (D + 2);
-        const float f = x[0] == -INFINITY ? (x[1] == 0.f ? 0.f : 1.f) : tc::ex2(x[0] - M);
-        L = fmaf(x[1], f, L);
-        A = fmaf(x[2 + e], f, A);
+    for (int k0 = 0; k0 < np; k0 += JOIN_BATCH) {
+        const int n = min(JOIN_BATCH, np - k0);
+        __syncthreads();
+        for (int k = e; k < n; k += D) {
+            float m, l;
+            ml(k0 + k, m, l, flag);
+            const float f = m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : tc::ex2(m - M);
+            s_f[k] = f;
+            L = fmaf(l, f, L);
+        }
+        __syncthreads();
+#pragma unroll 8
+        for (int k = 0; k < n; ++k) {
+            const int i = k0 + k;
+            const float x = i < ni ? s.own[((long long)i0 + i + u) * (D + 2) + 2 + e]
+                                   : s.pre[(((long long)j0 + i - ni + pu) * p.q_tile + row) * D + e];
+            A = fmaf(x, s_f[k], A);
+        }
     }
-    for (int j = j0; j <= j1; ++j) {
-        const float *ml = s.pre_ml + (j + pu) * 2 * p.q_tile + row;
-        const float f = ml[0] == -INFINITY ? (ml[p.q_tile] == 0.f ? 0.f : 1.f) : tc::ex2(ml[0] - M);
-        L = fmaf(ml[p.q_tile], f, L);
-        A = fmaf(s.pre[((j + pu) * p.q_tile + row) * D + e], f, A);
-    }
-    if (flag) L = __int_as_float(0x7fc00000);
+    L = group_sum<32>(L);
+    if (e % 32 == 0) s_red[1][e / 32] = L;
+    __syncthreads();
+    L = 0.f;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) L += s_red[1][i];
+    if (bad) L = __int_as_float(0x7fc00000);
     *out = from_f<T>(A / L);
 }
 

@@ -29,7 +29,6 @@
 // a single warp takes longer to issue a tile's MMAs than the tensor cores to do them.
 // Waits are bounded; one that gives up makes its pieces NaN and is reported.
 #include "paged.cuh"
-#include "rowvec.cuh"
 #include "runtime.cuh"
 #include "tc.cuh"
 
@@ -320,7 +319,7 @@ __global__ void __launch_bounds__(Cfg<D, GROUPS>::NT, 1)
         // and go on (every address is fixed, every barrier is still met): the pieces become NaN.
         const int grp = warp / 4, gt = tid % 128, c0 = grp * CN;
         const uint32_t lane_off = (uint32_t)(32 * (warp % 4)) << 16;
-        const F2 scale2 = f2(a.scale * LOG2E, a.scale * LOG2E), minus1 = f2(-1.f, -1.f);
+        const float scale2 = a.scale * LOG2E;
         bool gave_up = false;
         auto wait = [&](uint64_t *bar, uint32_t parity) {
             if (!mbar_try_wait(bar, parity) && !gave_up) gave_up = !mbar_wait(bar, parity, WAIT_LIMIT_NS);
@@ -338,16 +337,13 @@ __global__ void __launch_bounds__(Cfg<D, GROUPS>::NT, 1)
             const int ke = (int)min((long long)p.key_tiles, kb + (t1 - t));
             const int qt = u % p.q_tiles, h = u / p.q_tiles;
             const int nq = min(CN, a.B - qt * QT - c0);  // queries of this unit and group
-            F2 l[CN / 2];
+            float l[CN];
 #pragma unroll
-            for (int i = 0; i < CN / 2; ++i) l[i] = 0ull;
+            for (int i = 0; i < CN; ++i) l[i] = 0.f;
             for (int kt = kb; kt < ke; ++kt, ++n) {
                 const bool first = kt == kb, tail = (kt + 1) * KT > a.prefix_len;
                 const bool live = !tail || kt * KT + gt < a.prefix_len;
                 float v[CN], g = 0.f;
-                wait(&s_full[n & 1], (n >> 1) & 1);
-                fence_after_sync();
-                tmem_ld16(tbase + C::T_S + (n & 1) * QN + c0 + lane_off, v);
                 if (gate) {
                     wait(&g_full[gslot], gparity);
                     g = sG[gslot * KT + gt] * LOG2E;
@@ -356,25 +352,28 @@ __global__ void __launch_bounds__(Cfg<D, GROUPS>::NT, 1)
                         gparity ^= 1;
                     }
                 }
-                const F2 g2 = f2(g, g);
-                F2 z[CN / 2];
+                float z[CN];
                 auto minus_ref = [&]() {
 #pragma unroll
-                    for (int i = 0; i < CN / 2; i += 2) {
-                        const ulonglong2 m = *reinterpret_cast<const ulonglong2 *>(sM + c0 + 2 * i);
-                        z[i] = add2(z[i], m.x);
-                        z[i + 1] = add2(z[i + 1], m.y);
+                    for (int i = 0; i < CN; i += 4) {
+                        const float4 m = *reinterpret_cast<const float4 *>(sM + c0 + i);
+                        z[i] += m.x;
+                        z[i + 1] += m.y;
+                        z[i + 2] += m.z;
+                        z[i + 3] += m.w;
                     }
                 };
-                tmem_wait_ld_tied(v);
+                wait(&s_full[n & 1], (n >> 1) & 1);
+                fence_after_sync();
+                tmem_ld16_wait(tbase + C::T_S + (n & 1) * QN + c0 + lane_off, v);
                 fence_before_sync();
                 if (lane == 0) mbar_arrive(&s_empty[n & 1]);
                 auto logits = [&]() {
 #pragma unroll
-                    for (int i = 0; i < CN / 2; ++i) z[i] = fma2(f2(v[2 * i], v[2 * i + 1]), scale2, g2);
-                    if (!live) {  // the page's rows behind the prefix hold anything
+                    for (int i = 0; i < CN; ++i) z[i] = fmaf(v[i], scale2, g);
+                    if (tail) {  // the page's rows behind the prefix hold anything
 #pragma unroll
-                        for (int i = 0; i < CN / 2; ++i) z[i] = f2(-INFINITY, -INFINITY);
+                        for (int i = 0; i < CN; ++i) z[i] = live ? z[i] : -INFINITY;
                     }
                 };
                 logits();
@@ -382,23 +381,15 @@ __global__ void __launch_bounds__(Cfg<D, GROUPS>::NT, 1)
                 if (!first) {
                     minus_ref();
 #pragma unroll
-                    for (int i = 0; i < CN / 2; ++i) {
-                        float x, y;
-                        split(z[i], x, y);
-                        asm("max.f32 %0, %0, %1, %2;" : "+f"(top) : "f"(x), "f"(y));
-                    }
+                    for (int i = 0; i < CN; i += 2) asm("max.f32 %0, %0, %1, %2;" : "+f"(top) : "f"(z[i]), "f"(z[i + 1]));
                 }
                 if (group_any(grp, first || top > SLACK)) {
                     logits();
                     float mine = -INFINITY;
 #pragma unroll
-                    for (int i = 0; i < CN / 2; ++i) {
-                        float x, y;
-                        split(z[i], x, y);
-                        x = warp_max(x);
-                        y = warp_max(y);
-                        if (lane == 2 * i) mine = x;
-                        if (lane == 2 * i + 1) mine = y;
+                    for (int i = 0; i < CN; ++i) {
+                        const float x = warp_max(z[i]);
+                        if (lane == i) mine = x;
                     }
                     if (lane < CN) sR[(warp % 4) * QN + c0 + lane] = mine;
                     group_bar(grp);
@@ -415,7 +406,7 @@ __global__ void __launch_bounds__(Cfg<D, GROUPS>::NT, 1)
                         product_done(n - 1);
                         fence_after_sync();
 #pragma unroll
-                        for (int i = 0; i < CN / 2; ++i) l[i] = mul2(l[i], f2(sF[c0 + 2 * i], sF[c0 + 2 * i + 1]));
+                        for (int i = 0; i < CN; ++i) l[i] *= sF[c0 + i];
 #pragma unroll 1
                         for (int part = 0; part < 2; ++part) {  // hi, lo
                             const uint32_t at = tbase + C::T_O + part * QN + c0 + lane_off;
@@ -442,15 +433,12 @@ __global__ void __launch_bounds__(Cfg<D, GROUPS>::NT, 1)
                     uint32_t hi[4], lo[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        float x, y;
-                        split(z[4 * j + e], x, y);
-                        x = ex2(x);
-                        y = ex2(y);
-                        const F2 xy = f2(x, y);
-                        l[4 * j + e] = add2(l[4 * j + e], xy);
+                        const int i = 8 * j + 2 * e;
+                        const float x = ex2(z[i]), y = ex2(z[i + 1]);
+                        l[i] += x;
+                        l[i + 1] += y;
                         hi[e] = pack_bf16(x, y);
-                        split(fma2(f2(__uint_as_float(hi[e] << 16), __uint_as_float(hi[e] & 0xffff0000u)), minus1, xy), x, y);
-                        lo[e] = pack_bf16(x, y);
+                        lo[e] = pack_bf16(x - __uint_as_float(hi[e] << 16), y - __uint_as_float(hi[e] & 0xffff0000u));
                     }
                     *reinterpret_cast<uint4 *>(sP + (j ? hi1 : hi0)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                     *reinterpret_cast<uint4 *>(sP + (j ? lo1 : lo0)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -487,7 +475,7 @@ __global__ void __launch_bounds__(Cfg<D, GROUPS>::NT, 1)
                         if (i < nq) s.pre[(piece * QT + c0 + i) * D + dim] = v[i] + v2[i];
                 }
 #pragma unroll
-                for (int i = 0; i < CN / 2; ++i) split(l[i], v[2 * i], v[2 * i + 1]);
+                for (int i = 0; i < CN; ++i) v[i] = l[i];
                 const float sum = warp_sums(v);
                 if (lane < CN) sR[(warp % 4) * QN + c0 + lane] = sum;
             }

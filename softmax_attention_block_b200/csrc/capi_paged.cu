@@ -228,6 +228,8 @@ path_status path_pages_store(const void *k_cache, const void *v_cache, const flo
     a.H = H;
     a.capacity = capacity;
     a.row_bytes = d * (int)dtype_size((int)dt);
+    a.pages = (int)(((long long)capacity + page - 1) / page);
+    if (a.pages > max_pages) a.pages = max_pages;
     a.c = PagedCache{rows, n_slots, table, max_pages, nullptr, page_log2(page), n_pages, k_pages, v_pages, g_pages};
     a.tokens = tokens;
     a.info = info;

@@ -129,6 +129,7 @@ struct PagesStore {
     const void *k_cache, *v_cache;  // [B, H, capacity, d]
     const float *g_cache;           // [B, H, capacity]
     int B, H, capacity;
+    int pages;                      // pages of a full cache, at most max_pages
     int row_bytes;                  // d elements
     PagedCache c;                   // lens unused
     const int *tokens;              // [B]

@@ -147,35 +147,32 @@ __global__ void __launch_bounds__(TT) turn_kernel(PagedStep a, PagedScratch s, i
 // fp32 arithmetic on CUDA cores: 32 queries by 64 keys a tile, one pass over
 // the keys with a running maximum and sum. Thread (ty, tx) holds queries
 // 2 ty, 2 ty + 1 against keys tx + 16 i, then dims 4 tx + 64 i of their output.
+// Bound by shared-memory reads (10 of them for 32 products). Where a key's row
+// lies is looked up a tile ahead, so that the asynchronous copies of a tile wait
+// for nothing; a tile's keys come in under the former tile's values, its values
+// under its own keys.
 constexpr int QT = 32, KT = 64;
 
 template <int D>
 struct SimtCfg {
     static constexpr int LD = D + 4, LP = KT + 4;
     static constexpr int Q = 0, K = Q + QT * LD, V = K + KT * LD, P = V + KT * D, G = P + QT * LP;
-    static constexpr int SMEM = (G + KT) * 4;
+    static constexpr int SMEM = (G + 2 * KT) * 4;
 };
 
-// Rows of a key tile into shared memory; rows past the prefix are zero.
-template <int D>
-__device__ __forceinline__ bool load_tile(const void *pool, const PagedStep &a, int h, int key0, float *dst, int ld)
+// 16 bytes to shared memory, asynchronously; zeros where there is no source.
+__device__ __forceinline__ void copy16(void *dst, const void *src, bool there)
 {
-    constexpr int LPR = D / 4;
-    bool bad = false;
-    for (int i = threadIdx.x; i < KT * LPR; i += NT) {
-        const int r = i / LPR, x = i % LPR, key = key0 + r;
-        float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (key < a.prefix_len) {
-            const int p = a.prefix_table[key >> a.c.page_log2];
-            if (p >= 0 && p < a.c.n_pages)
-                f = static_cast<const float4 *>(pool)[((((long long)p * a.H + h) << a.c.page_log2) +
-                                                       (key & ((1 << a.c.page_log2) - 1))) * LPR + x];
-            else
-                bad = true;
-        }
-        *reinterpret_cast<float4 *>(dst + r * ld + 4 * x) = f;
-    }
-    return bad;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                 :
+                 : "r"(tc::smem_u32(dst)), "l"(src), "r"(there ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 template <int D>
@@ -184,18 +181,54 @@ __global__ void __launch_bounds__(NT) prefix_simt_kernel(PagedStep a, PagedScrat
     using C = SimtCfg<D>;
     constexpr int LD = C::LD, LP = C::LP, DV = D / 64;  // float4 columns a thread accumulates
     extern __shared__ float sm[];
+    __shared__ long long s_row[2][KT];  // row of the pool that a key of the tile is, or -1
     float *sQ = sm + C::Q, *sK = sm + C::K, *sV = sm + C::V, *sP = sm + C::P, *sG = sm + C::G;
     const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
     release_next();
-    wait_previous();
     const int q_rows = p.q_tiles * QT;
     const float scale2 = a.scale * LOG2E;
     const long long total = (long long)p.pre_units * p.key_tiles;
     const long long t0 = total * blockIdx.x / gridDim.x, t1 = total * (blockIdx.x + 1) / gridDim.x;
+    // where the keys of a tile lie, and their gate biases (-inf past the prefix)
+    auto look_up = [&](int h, int kt) {
+        bool bad = false;
+        if (tid < KT) {
+            const int key = kt * KT + tid;
+            long long row = -1;
+            float g = -INFINITY;
+            if (key < a.prefix_len) {
+                const int pg = a.prefix_table[key >> a.c.page_log2];
+                bad = pg < 0 || pg >= a.c.n_pages;
+                g = 0.f;
+                if (!bad) {
+                    row = (((long long)pg * a.H + h) << a.c.page_log2) + (key & ((1 << a.c.page_log2) - 1));
+                    if (a.c.g) g = a.c.g[row] * LOG2E;
+                }
+            }
+            s_row[kt & 1][tid] = row;
+            sG[(kt & 1) * KT + tid] = g;
+        }
+        return bad;
+    };
+    auto load = [&](const void *pool, int kt, float *dst, int ld) {
+        constexpr int LPR = D / 4;
+#pragma unroll
+        for (int i = tid; i < KT * LPR; i += NT) {
+            const int r = i / LPR, x = i % LPR;
+            const long long row = s_row[kt & 1][r];
+            copy16(dst + r * ld + 4 * x, static_cast<const float *>(pool) + (row < 0 ? 0 : row) * D + 4 * x, row >= 0);
+        }
+        copies_commit();
+    };
     for (long long t = t0; t < t1;) {
         const int u = (int)(t / p.key_tiles), kb = (int)(t % p.key_tiles);
         const int ke = (int)min((long long)p.key_tiles, kb + (t1 - t));
         const int qtile = u % p.q_tiles, h = u / p.q_tiles;
+        bool bad = look_up(h, kb);
+        __syncthreads();
+        load(a.c.k, kb, sK, LD);
+        load(a.c.v, kb, sV, D);
+        if (t == t0) wait_previous();  // the queries; keys and values are nobody's output
         for (int i = tid; i < QT * D; i += NT) {
             const int r = i / D, e = i % D, b = qtile * QT + r;
             sQ[r * LD + e] = b < a.B ? s.qt[((long long)h * q_rows + b) * D + e] : 0.f;
@@ -206,24 +239,12 @@ __global__ void __launch_bounds__(NT) prefix_simt_kernel(PagedStep a, PagedScrat
         for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int e = 0; e < DV; ++e) acc[i][e] = make_float4(0.f, 0.f, 0.f, 0.f);
-        bool bad = false;
         for (int kt = kb; kt < ke; ++kt) {
             const int key0 = kt * KT;
-            __syncthreads();  // the former tile is done with
-            bad |= load_tile<D>(a.c.k, a, h, key0, sK, LD);
-            bad |= load_tile<D>(a.c.v, a, h, key0, sV, D);
-            if (tid < KT) {
-                const int key = key0 + tid;
-                float g = -INFINITY;  // a key past the prefix
-                if (key < a.prefix_len) {
-                    const int pg = a.prefix_table[key >> a.c.page_log2];
-                    g = 0.f;
-                    if (a.c.g && pg >= 0 && pg < a.c.n_pages)
-                        g = a.c.g[(((long long)pg * a.H + h) << a.c.page_log2) + (key & ((1 << a.c.page_log2) - 1))] * LOG2E;
-                }
-                sG[tid] = g;
-            }
+            const float *g = sG + (kt & 1) * KT;
+            copies_wait<1>();  // the keys
             __syncthreads();
+            if (kt + 1 < ke) bad |= look_up(h, kt + 1);
             float z[2][4] = {};
 #pragma unroll 4
             for (int e = 0; e < D; e += 4) {
@@ -241,8 +262,7 @@ __global__ void __launch_bounds__(NT) prefix_simt_kernel(PagedStep a, PagedScrat
                 float mx = m[i];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float g = sG[tx + 16 * j];
-                    z[i][j] = key0 + tx + 16 * j < a.prefix_len ? fmaf(z[i][j], scale2, g) : -INFINITY;
+                    z[i][j] = key0 + tx + 16 * j < a.prefix_len ? fmaf(z[i][j], scale2, g[tx + 16 * j]) : -INFINITY;
                     mx = fmaxf(mx, z[i][j]);
                 }
 #pragma unroll
@@ -268,7 +288,9 @@ __global__ void __launch_bounds__(NT) prefix_simt_kernel(PagedStep a, PagedScrat
                     acc[i][e].w *= corr;
                 }
             }
-            __syncwarp();  // a warp's rows of P are its own
+            copies_wait<0>();  // the values
+            __syncthreads();   // and a warp's rows of P are its own
+            if (kt + 1 < ke) load(a.c.k, kt + 1, sK, LD);
 #pragma unroll 4
             for (int j = 0; j < KT; ++j) {
                 const float p0 = sP[(2 * ty) * LP + j], p1 = sP[(2 * ty + 1) * LP + j];
@@ -285,6 +307,8 @@ __global__ void __launch_bounds__(NT) prefix_simt_kernel(PagedStep a, PagedScrat
                     acc[1][e].w = fmaf(p1, v.w, acc[1][e].w);
                 }
             }
+            __syncthreads();
+            if (kt + 1 < ke) load(a.c.v, kt + 1, sV, D);
         }
         const long long piece = (long long)blockIdx.x + u;
         const bool any_bad = __syncthreads_or(bad);

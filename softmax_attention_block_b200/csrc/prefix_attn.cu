@@ -17,7 +17,6 @@ namespace path {
 
 namespace {
 
-constexpr int NT = 256;
 constexpr float LOG2E = 1.4426950408889634f;
 
 // One (batch row, head): G read once and written once, bound by HBM (8 d^2
@@ -144,19 +143,20 @@ __global__ void __launch_bounds__(TT) turn_kernel(PagedStep a, PagedScratch s, i
     }
 }
 
-// fp32 arithmetic on CUDA cores: 32 queries by 64 keys a tile, one pass over
-// the keys with a running maximum and sum. Thread (ty, tx) holds queries
-// 2 ty, 2 ty + 1 against keys tx + 16 i, then dims 4 tx + 64 i of their output.
-// Bound by shared-memory reads (10 of them for 32 products). Where a key's row
+// fp32 arithmetic on CUDA cores: QT queries (16 or 32) by 64 keys a tile, one pass
+// over the keys with a running maximum and sum. A warp holds four queries, a lane
+// two keys of the tile and then D / 32 dims of the output; queries and weights are
+// read as broadcasts. Bound by shared-memory reads (12 for 32 products of logits, 5
+// for 16 of outputs), or for few tiles by their latency. Where a key's row
 // lies is looked up a tile ahead, so that the asynchronous copies of a tile wait
 // for nothing; a tile's keys come in under the former tile's values, its values
 // under its own keys.
-constexpr int QT = 32, KT = 64;
+constexpr int KT = 64;
 
-template <int D>
+template <int D, int QT>
 struct SimtCfg {
-    static constexpr int LD = D + 4, LP = KT + 4;
-    static constexpr int Q = 0, K = Q + QT * LD, V = K + KT * LD, P = V + KT * D, G = P + QT * LP;
+    static constexpr int NT = 8 * QT, LD = D + 4;
+    static constexpr int Q = 0, K = Q + QT * LD, V = K + KT * LD, P = V + KT * D, G = P + QT * KT;
     static constexpr int SMEM = (G + 2 * KT) * 4;
 };
 
@@ -175,15 +175,24 @@ __device__ __forceinline__ void copies_wait()
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-template <int D>
-__global__ void __launch_bounds__(NT) prefix_simt_kernel(PagedStep a, PagedScratch s, PagedPlan p)
+// Largest value of a warp's lanes (NaN does not count).
+__device__ __forceinline__ float warp_max(float x)
 {
-    using C = SimtCfg<D>;
-    constexpr int LD = C::LD, LP = C::LP, DV = D / 64;  // float4 columns a thread accumulates
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+template <int D, int QT>
+__global__ void __launch_bounds__(SimtCfg<D, QT>::NT) prefix_simt_kernel(PagedStep a, PagedScratch s, PagedPlan p)
+{
+    using C = SimtCfg<D, QT>;
+    constexpr int LD = C::LD, NT = C::NT, DL = D / 32;  // dims a lane accumulates
     extern __shared__ float sm[];
     __shared__ long long s_row[2][KT];  // row of the pool that a key of the tile is, or -1
     float *sQ = sm + C::Q, *sK = sm + C::K, *sV = sm + C::V, *sP = sm + C::P, *sG = sm + C::G;
-    const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
+    const int tid = threadIdx.x, tx = tid % 32, ty = tid / 32;
+    float *sW = sP + ty * 4 * KT;  // this warp's weights: four queries of a key side by side
     release_next();
     const int q_rows = p.q_tiles * QT;
     const float scale2 = a.scale * LOG2E;
@@ -233,78 +242,76 @@ __global__ void __launch_bounds__(NT) prefix_simt_kernel(PagedStep a, PagedScrat
             const int r = i / D, e = i % D, b = qtile * QT + r;
             sQ[r * LD + e] = b < a.B ? s.qt[((long long)h * q_rows + b) * D + e] : 0.f;
         }
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-        float4 acc[2][DV];
+        float m[4], l[4], acc[4][DL];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 4; ++i) {
+            m[i] = -INFINITY;
+            l[i] = 0.f;
 #pragma unroll
-            for (int e = 0; e < DV; ++e) acc[i][e] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int e = 0; e < DL; ++e) acc[i][e] = 0.f;
+        }
         for (int kt = kb; kt < ke; ++kt) {
             const int key0 = kt * KT;
             const float *g = sG + (kt & 1) * KT;
             copies_wait<1>();  // the keys
             __syncthreads();
             if (kt + 1 < ke) bad |= look_up(h, kt + 1);
-            float z[2][4] = {};
-#pragma unroll 4
+            float z[4][2] = {};
+#pragma unroll 2
             for (int e = 0; e < D; e += 4) {
-                const float4 q0 = *reinterpret_cast<const float4 *>(sQ + (2 * ty) * LD + e);
-                const float4 q1 = *reinterpret_cast<const float4 *>(sQ + (2 * ty + 1) * LD + e);
+                const float4 k0 = *reinterpret_cast<const float4 *>(sK + tx * LD + e);
+                const float4 k1 = *reinterpret_cast<const float4 *>(sK + (tx + 32) * LD + e);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float4 k = *reinterpret_cast<const float4 *>(sK + (tx + 16 * j) * LD + e);
-                    z[0][j] = fmaf(q0.x, k.x, fmaf(q0.y, k.y, fmaf(q0.z, k.z, fmaf(q0.w, k.w, z[0][j]))));
-                    z[1][j] = fmaf(q1.x, k.x, fmaf(q1.y, k.y, fmaf(q1.z, k.z, fmaf(q1.w, k.w, z[1][j]))));
+                for (int i = 0; i < 4; ++i) {
+                    const float4 q = *reinterpret_cast<const float4 *>(sQ + (4 * ty + i) * LD + e);
+                    z[i][0] = fmaf(q.x, k0.x, fmaf(q.y, k0.y, fmaf(q.z, k0.z, fmaf(q.w, k0.w, z[i][0]))));
+                    z[i][1] = fmaf(q.x, k1.x, fmaf(q.y, k1.y, fmaf(q.z, k1.z, fmaf(q.w, k1.w, z[i][1]))));
                 }
             }
+            float w[2][4];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                float mx = m[i];
+            for (int i = 0; i < 4; ++i) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    z[i][j] = key0 + tx + 16 * j < a.prefix_len ? fmaf(z[i][j], scale2, g[tx + 16 * j]) : -INFINITY;
-                    mx = fmaxf(mx, z[i][j]);
-                }
-#pragma unroll
-                for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                for (int j = 0; j < 2; ++j)
+                    z[i][j] = key0 + tx + 32 * j < a.prefix_len ? fmaf(z[i][j], scale2, g[tx + 32 * j]) : -INFINITY;
+                const float mx = fmaxf(m[i], warp_max(fmaxf(z[i][0], z[i][1])));
                 const float base = mx == -INFINITY ? 0.f : mx;  // a row without a weight so far
                 const float corr = tc::ex2(m[i] - base);
-                float sum = 0.f;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float w = tc::ex2(z[i][j] - base);
-                    sP[(2 * ty + i) * LP + tx + 16 * j] = w;
-                    sum += w;
-                }
-#pragma unroll
-                for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                l[i] = fmaf(l[i], corr, sum);
+                for (int j = 0; j < 2; ++j) w[j][i] = tc::ex2(z[i][j] - base);
+                l[i] = fmaf(l[i], corr, w[0][i] + w[1][i]);  // of this lane's keys
                 m[i] = mx;
 #pragma unroll
-                for (int e = 0; e < DV; ++e) {
-                    acc[i][e].x *= corr;
-                    acc[i][e].y *= corr;
-                    acc[i][e].z *= corr;
-                    acc[i][e].w *= corr;
-                }
+                for (int e = 0; e < DL; ++e) acc[i][e] *= corr;
             }
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                *reinterpret_cast<float4 *>(sW + (tx + 32 * j) * 4) = make_float4(w[j][0], w[j][1], w[j][2], w[j][3]);
             copies_wait<0>();  // the values
-            __syncthreads();   // and a warp's rows of P are its own
+            __syncthreads();
             if (kt + 1 < ke) load(a.c.k, kt + 1, sK, LD);
 #pragma unroll 4
             for (int j = 0; j < KT; ++j) {
-                const float p0 = sP[(2 * ty) * LP + j], p1 = sP[(2 * ty + 1) * LP + j];
+                const float4 pw = *reinterpret_cast<const float4 *>(sW + j * 4);
+                const float *v = sV + j * D + DL * tx;
+                float x[DL];
+                if constexpr (DL == 4) {
+                    const float4 y = *reinterpret_cast<const float4 *>(v);
+                    x[0] = y.x;
+                    x[1] = y.y;
+                    x[2] = y.z;
+                    x[3] = y.w;
+                } else {
+                    const float2 y = *reinterpret_cast<const float2 *>(v);
+                    x[0] = y.x;
+                    x[1] = y.y;
+                }
 #pragma unroll
-                for (int e = 0; e < DV; ++e) {
-                    const float4 v = *reinterpret_cast<const float4 *>(sV + j * D + 4 * tx + 64 * e);
-                    acc[0][e].x = fmaf(p0, v.x, acc[0][e].x);
-                    acc[0][e].y = fmaf(p0, v.y, acc[0][e].y);
-                    acc[0][e].z = fmaf(p0, v.z, acc[0][e].z);
-                    acc[0][e].w = fmaf(p0, v.w, acc[0][e].w);
-                    acc[1][e].x = fmaf(p1, v.x, acc[1][e].x);
-                    acc[1][e].y = fmaf(p1, v.y, acc[1][e].y);
-                    acc[1][e].z = fmaf(p1, v.z, acc[1][e].z);
-                    acc[1][e].w = fmaf(p1, v.w, acc[1][e].w);
+                for (int e = 0; e < DL; ++e) {
+                    acc[0][e] = fmaf(pw.x, x[e], acc[0][e]);
+                    acc[1][e] = fmaf(pw.y, x[e], acc[1][e]);
+                    acc[2][e] = fmaf(pw.z, x[e], acc[2][e]);
+                    acc[3][e] = fmaf(pw.w, x[e], acc[3][e]);
                 }
             }
             __syncthreads();
@@ -313,18 +320,19 @@ __global__ void __launch_bounds__(NT) prefix_simt_kernel(PagedStep a, PagedScrat
         const long long piece = (long long)blockIdx.x + u;
         const bool any_bad = __syncthreads_or(bad);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int r = 2 * ty + i, b = qtile * QT + r;
+        for (int i = 0; i < 4; ++i) {
+            const int r = 4 * ty + i, b = qtile * QT + r;
+            const float sum = group_sum<32>(l[i]);
             if (b < a.B) {
-                float *o = s.pre + (piece * QT + r) * D;
+                float *o = s.pre + (piece * QT + r) * D + DL * tx;
 #pragma unroll
-                for (int e = 0; e < DV; ++e) *reinterpret_cast<float4 *>(o + 4 * tx + 64 * e) = acc[i][e];
+                for (int e = 0; e < DL; e += 2) *reinterpret_cast<float2 *>(o + e) = make_float2(acc[i][e], acc[i][e + 1]);
                 if (tx == 0) {
                     // the gate since the prefix's end weighs every key of it alike; where it
                     // leaves nothing (log f = -inf), neither the sum nor the values count
                     const float M = m[i] + s.qg[(long long)h * q_rows + b];
                     s.pre_ml[piece * 2 * QT + r] = M;
-                    s.pre_ml[piece * 2 * QT + QT + r] = M == -INFINITY && !isnan(l[i]) ? 0.f : l[i];
+                    s.pre_ml[piece * 2 * QT + QT + r] = M == -INFINITY && !isnan(sum) ? 0.f : sum;
                 }
             }
         }
@@ -333,13 +341,14 @@ __global__ void __launch_bounds__(NT) prefix_simt_kernel(PagedStep a, PagedScrat
     }
 }
 
-template <int D>
+template <int D, int QT>
 cudaError_t run_simt(const PagedStep &a, const PagedPlan &p, const PagedScratch &s, cudaStream_t st)
 {
-    auto k = prefix_simt_kernel<D>;
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SimtCfg<D>::SMEM);
+    using C = SimtCfg<D, QT>;
+    auto k = prefix_simt_kernel<D, QT>;
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
-    return launch_overlapped(k, p.pre_blocks, NT, SimtCfg<D>::SMEM, st, a, s, p);
+    return launch_overlapped(k, p.pre_blocks, C::NT, C::SMEM, st, a, s, p);
 }
 
 template <typename T, int D>
@@ -366,7 +375,8 @@ cudaError_t prefix_attn_simt(const PagedStep &a, int d, const PagedPlan &p,
                              const PagedScratch &s, cudaStream_t st)
 {
     Stage stage("prefix_attn", st);
-    return d == 64 ? run_simt<64>(a, p, s, st) : run_simt<128>(a, p, s, st);
+    if (p.q_tile == 16) return d == 64 ? run_simt<64, 16>(a, p, s, st) : run_simt<128, 16>(a, p, s, st);
+    return d == 64 ? run_simt<64, 32>(a, p, s, st) : run_simt<128, 32>(a, p, s, st);
 }
 
 }  // namespace path

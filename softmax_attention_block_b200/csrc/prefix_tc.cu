@@ -58,7 +58,7 @@ struct Cfg {
     static constexpr int K_OFF = 0, V_OFF = K_OFF + NK * TILE, Q_OFF = V_OFF + NV * TILE, P_OFF = Q_OFF + Q;
     static constexpr int G_OFF = P_OFF + NP * P, M_OFF = G_OFF + NG * KT * 4, F_OFF = M_OFF + QN * 4;
     static constexpr int RED_OFF = F_OFF + QN * 4, BAR_OFF = RED_OFF + 4 * QN * 4;
-    static constexpr int NBAR = 2 * NK + 2 * NV + NG + 11;
+    static constexpr int NBAR = 2 * NK + 2 * NV + 9;
     static constexpr int SMEM = BAR_OFF + NBAR * 8 + 16 + 1024;
     static constexpr int T_S = 0, T_O = 2 * QN, TMEM = 4 * QN;  // two S^T, then O^T for hi | lo
     static_assert(SMEM <= 232448, "shared memory");
@@ -122,11 +122,11 @@ __global__ void __launch_bounds__(Cfg<D, GROUPS>::NT, 1)
     extern __shared__ uint8_t smraw[];
     uint8_t *sm = smraw + (1024 - (smem_u32(smraw) & 1023)) % 1024;
     uint64_t *k_full = reinterpret_cast<uint64_t *>(sm + C::BAR_OFF), *k_empty = k_full + NK;
-    uint64_t *v_full = k_empty + NK, *v_empty = v_full + NV, *g_full = v_empty + NV;
-    uint64_t *q_full = g_full + NG, *q_empty = q_full + 1, *s_full = q_full + 2, *p_full = q_full + 4;
+    uint64_t *v_full = k_empty + NK, *v_empty = v_full + NV;
+    uint64_t *q_full = v_empty + NV, *q_empty = q_full + 1, *s_full = q_full + 2, *p_full = q_full + 4;
     // P and its product: a barrier for each parity of the tile, since one group may be a tile ahead
-    uint64_t *o_done = q_full + 6, *mma_done = q_full + 8, *s_empty = q_full + 9;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(q_full + 11);
+    uint64_t *o_done = q_full + 6, *mma_done = q_full + 8;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(q_full + 9);
     int *s_bad = reinterpret_cast<int *>(tmem_slot + 1);
     float *sG = reinterpret_cast<float *>(sm + C::G_OFF), *sM = reinterpret_cast<float *>(sm + C::M_OFF);
     float *sF = reinterpret_cast<float *>(sm + C::F_OFF), *sR = reinterpret_cast<float *>(sm + C::RED_OFF);
@@ -143,14 +143,11 @@ __global__ void __launch_bounds__(Cfg<D, GROUPS>::NT, 1)
             mbar_init(&v_full[i], 1);
             mbar_init(&v_empty[i], 1);
         }
-        for (int i = 0; i < NG; ++i) mbar_init(&g_full[i], 1);
         mbar_init(q_full, 1);
         mbar_init(q_empty, 1);
-        mbar_init(&s_full[0], 1);
-        mbar_init(&s_full[1], 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&p_full[i], 4 * GROUPS);  // a warp each
-            mbar_init(&s_empty[i], 4 * GROUPS);
+            mbar_init(&s_full[i], 2);  // the product, and the warp that issued it
             mbar_init(&o_done[i], 1);
         }
         mbar_init(mma_done, 2);
@@ -219,19 +216,15 @@ __global__ void __launch_bounds__(Cfg<D, GROUPS>::NT, 1)
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             if (lane == 0) {
-                if (cnt) mbar_expect_tx(&k_full[ks], cnt * box * D * 2);
+                // (a gate slot is free: tile n - NG = n - 1 - NV was done before V of tile n - 1 was loaded)
+                if (cnt) mbar_expect_tx(&k_full[ks], cnt * box * (D * 2 + (gate ? 4 : 0)));
                 else mbar_arrive(&k_full[ks]);
-                if (gate) {
-                    // the slot is free: tile n - NG = n - 1 - NV was done before V of tile n - 1 was loaded
-                    if (cnt) mbar_expect_tx(&g_full[gs], cnt * box * 4);
-                    else mbar_arrive(&g_full[gs]);
-                }
             }
             __syncwarp();
             if (good) {
                 for (int x = 0; x < PANELS; ++x)
                     tma_load_2d(sm + C::K_OFF + ks * C::TILE + x * KT * 128 + lane * box * 128, &mK, 64 * x, row, &k_full[ks]);
-                if (gate) bulk_load(sG + gs * KT + lane * box, a.c.g + row, box * 4, &g_full[gs]);
+                if (gate) bulk_load(sG + gs * KT + lane * box, a.c.g + row, box * 4, &k_full[ks]);
             }
             issued_k = n + 1;
             if (n >= NV && !mbar_wait(&v_empty[vs], (n / NV - 1) & 1, WAIT_LIMIT_NS)) ok = false;
@@ -249,10 +242,8 @@ __global__ void __launch_bounds__(Cfg<D, GROUPS>::NT, 1)
             issued_v = n + 1;
         }
         if (!ok) {  // leave no copy on its way into this block's memory
-            for (int n = max(0, issued_k - NK); n < issued_k; ++n) {
+            for (int n = max(0, issued_k - NK); n < issued_k; ++n)
                 mbar_wait(&k_full[n % NK], (n / NK) & 1, WAIT_LIMIT_NS);
-                if (gate && n >= issued_k - NG) mbar_wait(&g_full[n % NG], (n / NG) & 1, WAIT_LIMIT_NS);
-            }
             for (int n = max(0, issued_v - NV); n < issued_v; ++n)
                 mbar_wait(&v_full[n % NV], (n / NV) & 1, WAIT_LIMIT_NS);
             if (seg > 0) mbar_wait(q_full, (seg - 1) & 1, WAIT_LIMIT_NS);
@@ -269,7 +260,8 @@ __global__ void __launch_bounds__(Cfg<D, GROUPS>::NT, 1)
             const uint32_t ks = (uint32_t)n % NK;
             if (n == 0 || kt == 0) ok = mbar_wait(q_full, seg++ & 1, WAIT_LIMIT_NS);
             ok = ok && mbar_wait(&k_full[ks], (n / NK) & 1, WAIT_LIMIT_NS);
-            if (n >= 2) ok = ok && mbar_wait(&s_empty[n & 1], ((n >> 1) - 1) & 1, WAIT_LIMIT_NS);
+            // the buffer of S^T was read before the weights of tile n - 2 were complete
+            if (n >= 2) ok = ok && mbar_wait(&p_full[n & 1], ((n >> 1) - 1) & 1, WAIT_LIMIT_NS);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             fence_after_sync();
@@ -285,6 +277,12 @@ __global__ void __launch_bounds__(Cfg<D, GROUPS>::NT, 1)
             commit_if(issue, &k_empty[ks]);
             if (++kt == p.key_tiles) kt = 0;
             if (n + 1 == count || kt == 0) commit_if(issue, q_empty);
+            // A wait costs a softmax warp 150 cycles even where there is nothing to wait for, so this
+            // warp waits for them: tile n may be worked on once its logits are there, its gate biases
+            // (they came with the keys) and the buffer of its weights.
+            if (n >= NP) ok = mbar_wait(&o_done[(n - NP) & 1], ((n - NP) >> 1) & 1, WAIT_LIMIT_NS);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            if (lane == 0) mbar_arrive(&s_full[n & 1]);
         }
         // the tensor memory is freed after the issuing warps leave: no MMA may still be running then
         commit_if(issue, mma_done);
@@ -329,7 +327,7 @@ __global__ void __launch_bounds__(Cfg<D, GROUPS>::NT, 1)
         // this thread's row of P: chunk j of eight queries, hi and lo
         const uint32_t hi0 = sw128_offset(gt, c0), hi1 = sw128_offset(gt, c0 + 8);
         const uint32_t lo0 = QN == 32 ? sw128_offset(gt, 32 + c0) : C::PP + hi0, lo1 = QN == 32 ? sw128_offset(gt, 40 + c0) : C::PP + hi1;
-        uint32_t gslot = 0, gparity = 0;
+        uint32_t gslot = 0;
         int n = 0;
         while (n < count) {
             const long long t = t0 + n;
@@ -344,14 +342,6 @@ __global__ void __launch_bounds__(Cfg<D, GROUPS>::NT, 1)
                 const bool first = kt == kb, tail = (kt + 1) * KT > a.prefix_len;
                 const bool live = !tail || kt * KT + gt < a.prefix_len;
                 float v[CN], g = 0.f;
-                if (gate) {
-                    wait(&g_full[gslot], gparity);
-                    g = sG[gslot * KT + gt] * LOG2E;
-                    if (++gslot == NG) {
-                        gslot = 0;
-                        gparity ^= 1;
-                    }
-                }
                 float z[CN];
                 auto minus_ref = [&]() {
 #pragma unroll
@@ -364,10 +354,12 @@ __global__ void __launch_bounds__(Cfg<D, GROUPS>::NT, 1)
                     }
                 };
                 wait(&s_full[n & 1], (n >> 1) & 1);
+                if (gate) {
+                    g = sG[gslot * KT + gt] * LOG2E;
+                    if (++gslot == NG) gslot = 0;
+                }
                 fence_after_sync();
                 tmem_ld16_wait(tbase + C::T_S + (n & 1) * QN + c0 + lane_off, v);
-                fence_before_sync();
-                if (lane == 0) mbar_arrive(&s_empty[n & 1]);
                 auto logits = [&]() {
 #pragma unroll
                     for (int i = 0; i < CN; ++i) z[i] = fmaf(v[i], scale2, g);
@@ -424,9 +416,7 @@ __global__ void __launch_bounds__(Cfg<D, GROUPS>::NT, 1)
                     }
                     minus_ref();
                 }
-                // weights, split in two bf16 numbers; this thread's key is a row of P, whose buffer is
-                // free once the product of the tile that had it is done
-                if (n >= NP) product_done(n - NP);
+                // weights, split in two bf16 numbers; this thread's key is a row of P
                 uint8_t *sP = sm + C::P_OFF + (n % NP) * C::P;
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {

@@ -79,26 +79,22 @@ __device__ __forceinline__ bool group_any(int grp, bool x)
     return r != 0;
 }
 
-__device__ __forceinline__ float warp_max(float x)
+// Sum or maximum over the warp's lanes of each of 16 values; lane i gets the i % 16-th. Halves of
+// the values change places with halves of the lanes: 31 shuffles in all.
+template <bool SUM>
+__device__ __forceinline__ float warp_reduce(float (&v)[CN])
 {
-    float r;
-    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
-    return r;
-}
-
-// Sum over the warp's lanes of each of 16 values; lane i gets the i % 16-th.
-__device__ __forceinline__ float warp_sums(float (&v)[CN])
-{
+    auto both = [](float x, float y) { return SUM ? x + y : fmaxf(x, y); };
     const int lane = threadIdx.x % 32;
 #pragma unroll
-    for (int i = 0; i < CN; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], 16);
+    for (int i = 0; i < CN; ++i) v[i] = both(v[i], __shfl_xor_sync(0xffffffffu, v[i], 16));
 #pragma unroll
     for (int o = CN / 2; o > 0; o >>= 1) {
         const bool up = lane & o;
 #pragma unroll
         for (int i = 0; i < o; ++i) {
             const float send = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
-            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+            v[i] = both(keep, __shfl_xor_sync(0xffffffffu, send, o));
         }
     }
     return v[0];
@@ -147,7 +143,7 @@ __global__ void __launch_bounds__(Cfg<D, GROUPS>::NT, 1)
         mbar_init(q_empty, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&p_full[i], 4 * GROUPS);  // a warp each
-            mbar_init(&s_full[i], 2);  // the product, and the warp that issued it
+            mbar_init(&s_full[i], 3);  // the product, the warp that issued it, P's buffer
             mbar_init(&o_done[i], 1);
         }
         mbar_init(mma_done, 2);
@@ -277,12 +273,13 @@ __global__ void __launch_bounds__(Cfg<D, GROUPS>::NT, 1)
             commit_if(issue, &k_empty[ks]);
             if (++kt == p.key_tiles) kt = 0;
             if (n + 1 == count || kt == 0) commit_if(issue, q_empty);
-            // A wait costs a softmax warp 150 cycles even where there is nothing to wait for, so this
-            // warp waits for them: tile n may be worked on once its logits are there, its gate biases
-            // (they came with the keys) and the buffer of its weights.
-            if (n >= NP) ok = mbar_wait(&o_done[(n - NP) & 1], ((n - NP) >> 1) & 1, WAIT_LIMIT_NS);
-            if (!__all_sync(0xffffffffu, ok)) break;
-            if (lane == 0) mbar_arrive(&s_full[n & 1]);
+            // A wait costs a softmax warp 150 cycles even where there is nothing to wait for, so one
+            // stands for three: tile n may be worked on once its logits are there, its gate biases (they
+            // came with the keys, which this warp saw) and the buffer of its weights (free at first).
+            if (lane == 0) {
+                mbar_arrive(&s_full[n & 1]);
+                if (n < NP) mbar_arrive(&s_full[n & 1]);
+            }
         }
         // the tensor memory is freed after the issuing warps leave: no MMA may still be running then
         commit_if(issue, mma_done);
@@ -307,6 +304,7 @@ __global__ void __launch_bounds__(Cfg<D, GROUPS>::NT, 1)
             for (int kk = 0; kk < KT / 16; ++kk)
                 mma_ss_if(issue, tbase + C::T_O, vd + (kk * 2048 >> 4), pd + (kk * 2048 >> 4), id, !fresh || kk > 0);
             commit_if(issue, &v_empty[vs]);
+            commit_if(issue, &s_full[(n + NP) & 1]);  // tile n + NP may have this one's weights' place
             commit_if(issue, &o_done[n & 1]);
         }
         commit_if(issue, mma_done);
@@ -328,12 +326,10 @@ __global__ void __launch_bounds__(Cfg<D, GROUPS>::NT, 1)
         const uint32_t hi0 = sw128_offset(gt, c0), hi1 = sw128_offset(gt, c0 + 8);
         const uint32_t lo0 = QN == 32 ? sw128_offset(gt, 32 + c0) : C::PP + hi0, lo1 = QN == 32 ? sw128_offset(gt, 40 + c0) : C::PP + hi1;
         uint32_t gslot = 0;
-        int n = 0;
+        int n = 0, u = (int)(t0 / p.key_tiles), kb = (int)(t0 % p.key_tiles);
+        int h = u / p.q_tiles, qt = u % p.q_tiles;
         while (n < count) {
-            const long long t = t0 + n;
-            const int u = (int)(t / p.key_tiles), kb = (int)(t % p.key_tiles);
-            const int ke = (int)min((long long)p.key_tiles, kb + (t1 - t));
-            const int qt = u % p.q_tiles, h = u / p.q_tiles;
+            const int ke = min(p.key_tiles, kb + count - n);
             const int nq = min(CN, a.B - qt * QT - c0);  // queries of this unit and group
             float l[CN];
 #pragma unroll
@@ -377,12 +373,7 @@ __global__ void __launch_bounds__(Cfg<D, GROUPS>::NT, 1)
                 }
                 if (group_any(grp, first || top > SLACK)) {
                     logits();
-                    float mine = -INFINITY;
-#pragma unroll
-                    for (int i = 0; i < CN; ++i) {
-                        const float x = warp_max(z[i]);
-                        if (lane == i) mine = x;
-                    }
+                    const float mine = warp_reduce<false>(z);
                     if (lane < CN) sR[(warp % 4) * QN + c0 + lane] = mine;
                     group_bar(grp);
                     if (gt < CN) {
@@ -414,6 +405,7 @@ __global__ void __launch_bounds__(Cfg<D, GROUPS>::NT, 1)
                         }
                         tmem_wait_st();
                     }
+                    logits();
                     minus_ref();
                 }
                 // weights, split in two bf16 numbers; this thread's key is a row of P
@@ -451,6 +443,7 @@ __global__ void __launch_bounds__(Cfg<D, GROUPS>::NT, 1)
             }
             // the piece of this unit
             wait_previous();  // qg
+            const float qg = gt < nq ? s.qg[(long long)h * q_rows + qt * QT + c0 + gt] : 0.f;
             product_done(n - 1);
             fence_after_sync();
             const long long piece = (long long)blockIdx.x + u;
@@ -466,7 +459,7 @@ __global__ void __launch_bounds__(Cfg<D, GROUPS>::NT, 1)
                 }
 #pragma unroll
                 for (int i = 0; i < CN; ++i) v[i] = l[i];
-                const float sum = warp_sums(v);
+                const float sum = warp_reduce<true>(v);
                 if (lane < CN) sR[(warp % 4) * QN + c0 + lane] = sum;
             }
             const bool failed = group_any(grp, gave_up);
@@ -474,7 +467,7 @@ __global__ void __launch_bounds__(Cfg<D, GROUPS>::NT, 1)
                 // the gate since the prefix's end weighs every key of it alike; where it leaves
                 // nothing (log f = -inf), neither the sum nor the values count
                 const int c = c0 + gt;
-                const float M = s.qg[(long long)h * q_rows + qt * QT + c] - sM[c];
+                const float M = qg - sM[c];
                 const float L = (sR[c] + sR[QN + c]) + (sR[2 * QN + c] + sR[3 * QN + c]);
                 s.pre_ml[piece * 2 * QT + c] = M;
                 s.pre_ml[piece * 2 * QT + QT + c] = M == -INFINITY && !isnan(L) ? 0.f : L;
@@ -482,6 +475,12 @@ __global__ void __launch_bounds__(Cfg<D, GROUPS>::NT, 1)
             if (gt == 0)
                 s.pre_flag[4 * piece + grp] = (failed ? PIECE_GAVE_UP : 0) | (*(volatile int *)s_bad ? PIECE_BAD_PAGE : 0);
             group_bar(grp);
+            kb = 0;
+            ++u;
+            if (++qt == p.q_tiles) {
+                qt = 0;
+                ++h;
+            }
         }
     }
     fence_before_sync();

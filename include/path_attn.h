@@ -295,8 +295,8 @@ path_status path_attn_prefill(const void *q, const void *k, const void *v, const
  * as each call says. Two calls on one pool or table, or with one workspace, have to be
  * ordered (one stream, or events).
  * page is a power of two from 16 to 1024; d in {64, 128}; dt PATH_F32 or PATH_BF16;
- * n_pages * H * page, n_slots * max_pages and max_pages * page below 2^31;
- * B * H <= 65535; at most 4096 rows in a reserve or fork. Beyond these:
+ * n_pages * H * page and n_slots * max_pages below 2^31; max_pages * page and a prefix
+ * at most 2^30 rows; B * H <= 65535; at most 4096 rows in a reserve or fork. Beyond these:
  * PATH_ERR_UNSUPPORTED.
  */
 
@@ -330,8 +330,8 @@ path_status path_decode_step_paged(const void *q, const void *k_new, const void 
 /*
  * The same for sequences that all continue one prefix of prefix_len >= 1 rows, whose
  * attention is computed once for the whole batch. The prefix's pages (prefix_table:
- * ceil(prefix_len / page) pages of the same pool, e.g. the prefix slot's row of table)
- * are only read: its keys p_j and gate biases g_j stay as they were when it ended.
+ * ceil(prefix_len / page) pages of the same pool, best the prefix slot's own row of table,
+ * which a compaction keeps up to date) are only read: its keys p_j and gate biases g_j stay as they were when it ended.
  * Instead each slot carries
  *   state   [n_slots, H, d, d] fp32, G = H_t ... H_{P+1}, the product of the Householder
  *           factors since the prefix ended (row-major; identity at its end),
@@ -341,7 +341,9 @@ path_status path_decode_step_paged(const void *q, const void *k_new, const void 
  * since q^T (G p_j) = (G^T q)^T p_j. path_state_copy sets a slot to the identity.
  * The own rows, lens, errors and everything else as path_decode_step_paged; an
  * out-of-range page of the prefix makes every row NaN. The prefix's pages must not be
- * among the pages of the batch's slots.
+ * among the pages of the batch's slots. PATH_BF16: queries turned back and weights meet the
+ * prefix on the tensor cores as sums of two bf16 numbers (off by 2^-17), so an infinite key
+ * or value of the prefix may turn into NaN.
  */
 path_status path_decode_step_shared(const void *q, const void *k_new, const void *v_new, const void *w,
                                     const float *beta, const float *log_f, float scale, int B, int H,

@@ -185,6 +185,22 @@ def _check_dev(*ts):
                          f"torch.cuda.device({ts[0].device})")
 
 
+def _check_here(*ts):
+    """_check_dev, its usual outcome first: contiguous tensors on the current device."""
+    here = torch.cuda.current_device() if torch.cuda.is_initialized() else -1
+    for t in ts:
+        if t is not None and (t.get_device() != here or here < 0 or not t.is_contiguous()):
+            return _check_dev(*ts)
+
+
+def _room(nbytes, ws, device):
+    """A workspace of nbytes() bytes, or the caller's, whose size the library checks."""
+    if ws is None:
+        n = nbytes()
+        return torch.empty(max(n, 1), dtype=torch.uint8, device=device), n
+    return ws, ws.nbytes
+
+
 def _check_attn_inputs(q, k, v, w, beta, log_f):
     if q.dim() != 4:
         raise ValueError("q must be [B,H,L,d]")
@@ -198,7 +214,7 @@ def _check_attn_inputs(q, k, v, w, beta, log_f):
 
 
 def _stream():
-    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _workspace(nbytes, device, ws):
@@ -439,20 +455,24 @@ def path_test_withhold_kv_load(on: bool) -> None:
 
 # ---------------------------------------------------------------- the paged decode cache
 def _expect_pool(k_pages, v_pages, g_pages):
-    if k_pages.dim() != 4 or k_pages.dtype not in _DT:
+    shape = k_pages.shape
+    if len(shape) != 4 or k_pages.dtype not in _DT:
         raise ValueError("k_pages must be [n_pages,H,page,d], float32 or bfloat16")
-    _expect("v_pages", v_pages, k_pages.shape, k_pages.dtype)
-    _expect("g_pages", g_pages, k_pages.shape[:3], torch.float32)
-    return k_pages.shape
+    _expect("v_pages", v_pages, shape, k_pages.dtype)
+    if g_pages is not None:
+        _expect("g_pages", g_pages, shape[:3], torch.float32)
+    return shape
 
 
 def _expect_table(table, **per_slot):
-    if table.dim() != 2:
+    shape = table.shape
+    if len(shape) != 2:
         raise ValueError("table must be [n_slots,max_pages]")
-    _expect("table", table, table.shape, torch.int32)
+    _expect("table", table, shape, torch.int32)
+    slots = shape[:1]
     for n, t in per_slot.items():
-        _expect(n, t, table.shape[:1], torch.int32)
-    return table.shape
+        _expect(n, t, slots, torch.int32)
+    return shape
 
 
 def _expect_owner(owner):
@@ -464,13 +484,13 @@ def _expect_owner(owner):
 
 def _expect_list(**lists):
     """int32 lists of one length; returns it."""
-    n = None
+    shape = None
     for name, t in lists.items():
         if t.dim() != 1:
             raise ValueError(f"{name}: must have one dimension")
-        n = t.shape[0] if n is None else n
-        _expect(name, t, (n,), torch.int32)
-    return n
+        shape = shape or t.shape
+        _expect(name, t, shape, torch.int32)
+    return shape[0]
 
 
 def _moves(moves, most, device):
@@ -505,8 +525,9 @@ def _step_paged(where, q, k_new, v_new, w, beta, k_pages, v_pages, table, lens, 
         out = torch.empty_like(q) if rows is None else torch.zeros_like(q)
     if (log_f is None) != (g_pages is None):
         raise ValueError("log_f and g_pages go together")
+    shape = (B, H, d)
     for n, t in (("q", q), ("k_new", k_new), ("v_new", v_new), ("w", w), ("out", out)):
-        _expect(n, t, (B, H, d), dtype)
+        _expect(n, t, shape, dtype)
     _expect("beta", beta, (B, H), torch.float32)
     _expect("log_f", log_f, (B, H), torch.float32)
     n_slots, max_pages = _expect_table(table, lens=lens)
@@ -525,10 +546,10 @@ def _step_paged(where, q, k_new, v_new, w, beta, k_pages, v_pages, table, lens, 
         _expect("g_state", g_state, (n_slots, H), torch.float32)
         more = (prefix_table, state, g_state)
         extra = (_ptr(prefix_table), prefix_len, _ptr(state), _ptr(g_state))
-    _check_dev(q, k_new, v_new, w, beta, log_f, k_pages, v_pages, g_pages, table, lens, rows, out,
+    _check_here(q, k_new, v_new, w, beta, log_f, k_pages, v_pages, g_pages, table, lens, rows, out,
                workspace, *more)
-    nbytes = path_decode_paged_workspace_bytes(B, H, max_pages, page, d, dtype, prefix_len)
-    ws = _workspace(nbytes, q.device, workspace)
+    ws, nbytes = _room(lambda: path_decode_paged_workspace_bytes(B, H, max_pages, page, d, dtype, prefix_len),
+                       workspace, q.device)
     st = getattr(lib(), where)(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(w), _ptr(beta), _ptr(log_f),
                                _scale(scale, d), B, H, d, _DT[dtype], _ptr(k_pages), _ptr(v_pages),
                                _ptr(g_pages), n_pages, page, _ptr(table), n_slots, max_pages,
@@ -569,7 +590,7 @@ def path_pages_reserve(table, held, owner, page, rows, tokens, info=None):
     n_slots, max_pages = _expect_table(table, held=held)
     n_pages, n = _expect_owner(owner), _expect_list(rows=rows, tokens=tokens)
     info = _info(info, table.device)
-    _check_dev(table, held, owner, rows, tokens, info)
+    _check_here(table, held, owner, rows, tokens, info)
     st = lib().path_pages_reserve(_ptr(table), _ptr(held), _ptr(owner), n_slots, max_pages, n_pages,
                                   int(page), _ptr(rows), _ptr(tokens), n, _ptr(info), _stream())
     if st:
@@ -585,7 +606,7 @@ def path_pages_fork(table, held, lens, owner, page, parents, children, moves=Non
     n_pages, n = _expect_owner(owner), _expect_list(parents=parents, children=children)
     moves, most = _moves(moves, min(n * max_pages, n_pages), table.device)
     info = _info(info, table.device)
-    _check_dev(table, held, lens, owner, parents, children, moves, info)
+    _check_here(table, held, lens, owner, parents, children, moves, info)
     st = lib().path_pages_fork(_ptr(table), _ptr(held), _ptr(lens), _ptr(owner), n_slots, max_pages,
                                n_pages, int(page), _ptr(parents), _ptr(children), n, _ptr(moves),
                                most, _ptr(info), _stream())
@@ -598,7 +619,7 @@ def path_pages_free(table, held, lens, owner, rows):
     """Frees the slots' pages: their entries and owners become -1, held and lens 0."""
     n_slots, max_pages = _expect_table(table, held=held, lens=lens)
     n_pages, n = _expect_owner(owner), _expect_list(rows=rows)
-    _check_dev(table, held, lens, owner, rows)
+    _check_here(table, held, lens, owner, rows)
     st = lib().path_pages_free(_ptr(table), _ptr(held), _ptr(lens), _ptr(owner), n_slots, max_pages,
                                n_pages, _ptr(rows), n, _stream())
     if st:
@@ -612,7 +633,7 @@ def path_pages_compact(table, held, owner, moves=None, info=None):
     n_pages = _expect_owner(owner)
     moves, most = _moves(moves, n_pages // 2, table.device)
     info = _info(info, table.device)
-    _check_dev(table, held, owner, moves, info)
+    _check_here(table, held, owner, moves, info)
     st = lib().path_pages_compact(_ptr(table), _ptr(held), _ptr(owner), n_slots, max_pages, n_pages,
                                   _ptr(moves), most, _ptr(info), _stream())
     if st:
@@ -625,7 +646,7 @@ def path_pages_copy(moves, info, k_pages, v_pages, g_pages=None):
     n_pages, H, page, d = _expect_pool(k_pages, v_pages, g_pages)
     moves, most = _moves(moves, 0, k_pages.device)
     _expect("info", info, (4,), torch.int32)
-    _check_dev(moves, info, k_pages, v_pages, g_pages)
+    _check_here(moves, info, k_pages, v_pages, g_pages)
     st = lib().path_pages_copy(_ptr(moves), most, _ptr(info), _ptr(k_pages), _ptr(v_pages),
                                _ptr(g_pages), n_pages, H, page, d, _DT[k_pages.dtype], _stream())
     if st:
@@ -650,7 +671,7 @@ def path_pages_store(k_cache, v_cache, k_pages, v_pages, table, rows, tokens, g_
     _expect("rows", rows, (B,), torch.int32)
     _expect("tokens", tokens, (B,), torch.int32)
     _expect("info", info, (4,), torch.int32)
-    _check_dev(k_cache, v_cache, g_cache, k_pages, v_pages, g_pages, table, rows, tokens, info)
+    _check_here(k_cache, v_cache, g_cache, k_pages, v_pages, g_pages, table, rows, tokens, info)
     st = lib().path_pages_store(_ptr(k_cache), _ptr(v_cache), _ptr(g_cache), B, H, d, capacity,
                                 _DT[k_pages.dtype], _ptr(k_pages), _ptr(v_pages), _ptr(g_pages),
                                 n_pages, page, _ptr(table), n_slots, max_pages, _ptr(rows),
@@ -668,7 +689,7 @@ def path_state_copy(state, parents, children, g_state=None):
     _expect("state", state, (n_slots, H, d, d), torch.float32)
     _expect("g_state", g_state, (n_slots, H), torch.float32)
     n = _expect_list(parents=parents, children=children)
-    _check_dev(state, g_state, parents, children)
+    _check_here(state, g_state, parents, children)
     st = lib().path_state_copy(_ptr(state), _ptr(g_state), n_slots, H, d, _ptr(parents),
                                _ptr(children), n, _stream())
     if st:

@@ -28,11 +28,13 @@ int page_log2(int page)
 
 bool aligned(const void *p, unsigned bytes) { return !(reinterpret_cast<uintptr_t>(p) & (bytes - 1)); }
 
-// Row and entry numbers stay within 31 bits.
+// Row and entry numbers stay within 31 bits, a sequence's own with room for a tile behind it.
+constexpr int MAX_ROWS = 1 << 30;  // of one sequence or prefix
+
 bool pool_fits(int n_pages, int H, int page) { return (long long)n_pages * H * page < (1LL << 31); }
 bool table_fits(int n_slots, int max_pages, int page)
 {
-    return (long long)n_slots * max_pages < (1LL << 31) && (long long)max_pages * page < (1LL << 31);
+    return (long long)n_slots * max_pages < (1LL << 31) && (long long)max_pages * page <= MAX_ROWS;
 }
 
 // Whether a table of this shape and its page size can be worked on.
@@ -83,7 +85,7 @@ extern "C" {
 size_t path_decode_paged_workspace_bytes(int B, int H, int max_pages, int page, int d, path_dtype dt,
                                          int prefix_len)
 {
-    if (B <= 0 || H <= 0 || max_pages <= 0 || prefix_len < 0 || page_log2(page) < 0 ||
+    if (B <= 0 || H <= 0 || max_pages <= 0 || prefix_len < 0 || prefix_len > MAX_ROWS || page_log2(page) < 0 ||
         !table_fits(1, max_pages, page) || (d != 64 && d != 128) || !kv_dtype_ok(dt) ||
         (long long)B * H > 65535)
         return 0;
@@ -125,6 +127,7 @@ path_status path_decode_step_shared(const void *q, const void *k_new, const void
     const path_status st = step_args(q, k_new, v_new, w, beta, log_f, scale, B, H, d, dt, k_pages, v_pages,
                                      g_pages, n_pages, page, table, n_slots, max_pages, lens, rows, out, a);
     if (st != PATH_OK) return st;
+    if (prefix_len > MAX_ROWS) return PATH_ERR_UNSUPPORTED;
     if (!aligned(state, 16)) return PATH_ERR_INVALID_ARG;
     a.prefix_table = prefix_table;
     a.prefix_len = prefix_len;

@@ -139,8 +139,13 @@ struct Cursor {
         left -= UNIT_COST;
         if (left <= 0 || ++h < a.H) return;
         h = 0;
-        do at_row<GR>(a.c, b + 1);  // a row with granules follows, for something is left
-        while (nt == 0);
+        do {  // a row with granules follows, for something is left
+            if (b + 1 >= a.B) {  // unless the lengths changed meanwhile
+                left = 0;
+                return;
+            }
+            at_row<GR>(a.c, b + 1);
+        } while (nt == 0);
     }
 };
 
@@ -639,22 +644,25 @@ __global__ void __launch_bounds__(NT) decode_join_kernel(PagedStep a, PagedScrat
     *out = from_f<T>(A / L);
 }
 
+template <typename T, int D, bool GATE, bool SHARED>
+cudaError_t run_own(const PagedStep &a, const PagedPlan &p, const PagedScratch &s, cudaStream_t st)
+{
+    auto k = decode_own_kernel<T, D, GATE, SHARED>;
+    constexpr int smem = OwnCfg<T, D>::SMEM;
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    if (SHARED) return launch_overlapped(k, p.own_blocks, NT, smem, st, a, s);
+    k<<<p.own_blocks, NT, smem, st>>>(a, s);
+    count_launches();
+    return cudaGetLastError();
+}
+
 template <typename T, int D, bool SHARED>
 cudaError_t run(const PagedStep &a, const PagedPlan &p, const PagedScratch &s, cudaStream_t st)
 {
     {
         Stage stage("decode_own", st);
-        auto k = a.c.g ? decode_own_kernel<T, D, true, SHARED> : decode_own_kernel<T, D, false, SHARED>;
-        constexpr int smem = OwnCfg<T, D>::SMEM;
-        cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
-        if (SHARED) {
-            e = launch_overlapped(k, p.own_blocks, NT, smem, st, a, s);
-        } else {
-            k<<<p.own_blocks, NT, smem, st>>>(a, s);
-            count_launches();
-            e = cudaGetLastError();
-        }
+        cudaError_t e = a.c.g ? run_own<T, D, true, SHARED>(a, p, s, st) : run_own<T, D, false, SHARED>(a, p, s, st);
         if (e != cudaSuccess) return e;
     }
     Stage stage("decode_join", st);

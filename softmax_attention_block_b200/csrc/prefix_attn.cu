@@ -346,7 +346,7 @@ cudaError_t run_simt(const PagedStep &a, const PagedPlan &p, const PagedScratch 
 {
     using C = SimtCfg<D, QT>;
     auto k = prefix_simt_kernel<D, QT>;
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     return launch_overlapped(k, p.pre_blocks, C::NT, C::SMEM, st, a, s, p);
 }

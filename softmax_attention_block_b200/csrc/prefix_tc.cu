@@ -501,7 +501,7 @@ cudaError_t run(const PagedStep &a, const PagedPlan &p, const PagedScratch &s, c
         !make_map_2d(&mV, a.c.v, BF16, D, rows, page < KT ? page : KT))
         return cudaErrorInvalidValue;
     auto k = prefix_tc_kernel<D, GROUPS>;
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     return launch_overlapped(k, p.pre_blocks, C::NT, C::SMEM, st, mQ, mK, mV, a, s, p);
 }

@@ -121,12 +121,12 @@ class Cache:
                                              g_state=self.gs, **kw)
         return P.path_decode_step_paged(*args, **kw)
 
-    def check(self, before, x, out, skip=()):
+    def check(self, before, x, out, skip=(), scale=None):
         """One step from the pool as it was (`before`: clones of k, v, g, state, gs) to the pool
         and out as they are now."""
         H, d, page, half = self.H, self.d, self.page, HALF[self.dtype]
         k0, v0, g0, s0, gs0 = before
-        scale = d ** -0.5
+        scale = d ** -0.5 if scale is None else scale
         ek, ev = k0.clone(), v0.clone()  # what nothing may change is as it was
         eg = g0.clone() if g0 is not None else None
         lens = self.lens.tolist()
@@ -180,7 +180,7 @@ class Cache:
             a = torch.softmax(z, -1)
             ref = (a.unsqueeze(1) @ vals).squeeze(1)
             zmax = z[torch.isfinite(z)].abs().max()
-            ez = scale * qk * (8 * math.sqrt(d) * 2.0 ** -24 + 2 * two) + 4 * zmax * 2.0 ** -24
+            ez = abs(scale) * qk * (8 * math.sqrt(d) * 2.0 ** -24 + 2 * two) + 4 * zmax * 2.0 ** -24
             vmax = vals.abs().amax((1, 2))
             tol = half * ref.abs() + (2 * vmax * (ez + two + 2.0 ** -20)).unsqueeze(-1)
             err = (out[b].double() - ref).abs()
@@ -243,6 +243,8 @@ PREFIX = [
     (1000, [5, 70, 0, 64, 200], 5, 64, True),
     (5003, [i % 9 for i in range(70)], 3, 64, False),
     (300, [2] * 130, 1, 256, True),
+    (2500, [3, 0], 1, 1024, False),
+    (77, [i % 5 for i in range(600)], 1, 16, False),
 ]
 
 
@@ -283,6 +285,56 @@ def test_lowest_values_infinities_and_nan(P, prefix):
     out = c.call(P, x)
     assert torch.equal(out[:, 0], x["v_new"][:, 0])
     assert torch.isnan(out[0, 2]).all() and torch.isfinite(out[1]).all() and torch.isfinite(out[0, :2]).all()
+
+
+@pytest.mark.parametrize("prefix", [0, 200])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("scale", [0.0, -0.3, 1.5])
+def test_scales(P, scale, dtype, prefix):
+    c = Cache([30, 0, 100], 2, 64, 32, dtype, prefix > 0, prefix=prefix, seed=6)
+    before, x = c.snap(), c.step_inputs()
+    out = c.call(P, x, scale=scale)
+    c.check(before, x, out, scale=scale)
+
+
+@pytest.mark.parametrize("B", [5, 20, 40, 64])
+@pytest.mark.parametrize("d,dtype,gate", [(64, BF, True), (128, BF, False), (64, F32, False), (128, F32, True)])
+def test_a_maximum_that_keeps_rising(P, B, d, dtype, gate):
+    """Keys that grow along the prefix: the running maximum moves many times, over many tiles of a
+    block and from one head to the next."""
+    H, n, page = 24, 9000, 64
+    c = Cache([i % 3 for i in range(B)], H, d, page, dtype, gate, seed=B, prefix=n)
+    for j, p in enumerate(c.pages(None)):
+        c.k[p] *= 0.05 + 3.0 * j * page / n
+    before, x = c.snap(), c.step_inputs()
+    out = c.call(P, x, scale=0.7)
+    c.check(before, x, out, scale=0.7)
+
+
+@pytest.mark.parametrize("prefix", [0, 130])
+def test_a_captured_step_serves_growing_sequences(P, prefix):
+    """Lengths are read on the device: one graph is every step, until a page is missing."""
+    kw = dict(gate=True, seed=12, prefix=prefix)
+    c, e = (Cache([14, 40], 2, 64, 16, BF, **kw) for _ in range(2))
+    x = c.step_inputs()
+    ws = torch.empty(P.path_decode_paged_workspace_bytes(2, 2, c.M, 16, 64, BF, prefix), dtype=torch.uint8,
+                     device="cuda")
+    out = torch.zeros_like(x["q"])
+    rows, ones = ints(c.slot), torch.ones_like(c.lens)
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        c.call(P, x, out=out, workspace=ws, rows=rows)
+        c.lens += ones
+    for step in range(4):  # row 0 fills its page at 16 and has no other
+        gr.replay()
+        want = e.call(P, x, rows=rows)
+        e.lens += ones
+        assert torch.equal(out[1], want[1])
+        if step < 2:
+            assert torch.equal(out, want)
+            assert P.path_attn_wait_status(ws) == 0
+        else:
+            assert torch.isnan(out[0]).all() and P.path_attn_wait_status(ws) == PAGE_ERR
 
 
 @pytest.mark.parametrize("prefix", [0, 50])

@@ -73,12 +73,13 @@ def test_step_refusals(lib, shared):
     assert step(lib, shared, ws=FAKE, wsb=100) == WORKSPACE
     assert step(lib, shared, ws=FAKE + 16) == INVALID
     for bad in (dict(page=24), dict(page=8), dict(page=2048), dict(d=32), dict(dt=MIXED), dict(B=70000),
-                dict(N=1 << 30), dict(R=1 << 30, M=4), dict(M=1 << 28)):
+                dict(N=1 << 30), dict(R=1 << 30, M=4), dict(M=(1 << 26) + 1)):
         assert step(lib, shared, **bad) == UNSUPPORTED, bad
     if shared:
         for bad in (dict(pt=None), dict(plen=0), dict(plen=-1), dict(state=None), dict(state=FAKE + 4),
                     dict(gs=FAKE), dict(log_f=FAKE, g=FAKE)):
             assert step(lib, shared, **bad) == INVALID, bad
+        assert step(lib, shared, plen=(1 << 30) + 1) == UNSUPPORTED
 
 
 def test_table_refusals(lib):

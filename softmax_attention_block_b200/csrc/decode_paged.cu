@@ -21,26 +21,32 @@ namespace path {
 
 namespace {
 
-constexpr int NT = 256, WARPS = NT / 32;
 constexpr float LOG2E = 1.4426950408889634f;
 
 // A warp's granule: GR rows of K and V (and gate biases) of one head, always inside one page.
 // LPR lanes hold a row, 16 elements each as CPL 16-byte chunks; a pass takes 32 / LPR rows.
 template <typename T, int D>
 struct OwnCfg {
+    // Warps of a block, and how many of them work when there is much to do. Rows of 128 bytes take
+    // more instructions a byte, and the shares of short sequences wait for one another: twelve warps
+    // instead of eight there (109 us instead of 117 for 96 rows of 0 to 512 tokens behind a prefix, 24
+    // heads of 64). Long shares are bound by HBM, whose rate falls with the number of streams (283 us
+    // instead of 246 for 48 rows of 500 to 6000). Even at about 45 granules for each of eight warps.
+    static constexpr int WARPS = D * sizeof(T) == 128 ? 12 : 8, FEW = 8, NT = 32 * WARPS;
+    static constexpr int LONG_SHARE = 40;
     static constexpr int LPR = D / 16, RPP = 32 / LPR;
     static constexpr int GR = own_granule(D, sizeof(T));
     static constexpr int PASSES = GR / RPP;
     static constexpr int CPL = sizeof(T);
     static constexpr int ROW_CHUNKS = D * (int)sizeof(T) / 16;
     static constexpr int TILE = GR * D * (int)sizeof(T);
-    static constexpr int STAGES = 24576 / (2 * TILE);
+    static constexpr int STAGES = 196608 / WARPS / (2 * TILE), MORE_STAGES = 196608 / FEW / (2 * TILE);  // of a warp
     static constexpr int GATE = GR * 4;
     static constexpr int ROW = D * (int)sizeof(T);
-    // shared memory of a warp: a ring of key and value tiles, its units' q and w, its gate biases
-    static constexpr int RING = STAGES * 2 * TILE, HEAD = STAGES * 2 * ROW;
-    static constexpr int SMEM = WARPS * (RING + HEAD + STAGES * GATE);
-    static_assert(GR % RPP == 0 && STAGES >= 2 && TILE % 128 == 0, "granule");
+    // shared memory: the warps' rings of key and value tiles, then their units' q and w, then gate biases
+    static constexpr int SLOTS = WARPS * STAGES > FEW * MORE_STAGES ? WARPS * STAGES : FEW * MORE_STAGES;
+    static constexpr int SMEM = SLOTS * (2 * TILE + 2 * ROW + GATE);
+    static_assert(GR % RPP == 0 && STAGES >= 3 && TILE % 128 == 0, "granule");
 };
 
 // Starting and ending a unit (one head of one batch row) takes a warp about as long as one
@@ -58,6 +64,7 @@ __device__ __forceinline__ int cost_of(const PagedCache &c, int b)
     return n < 0 ? 0 : n / GR + 1 + UNIT_COST;
 }
 
+template <int WARPS>
 __device__ long long block_scan(long long x, long long *total)
 {
     __shared__ long long s_w[WARPS];
@@ -159,15 +166,15 @@ struct Piece {
 enum { FIRST = 1, LAST = 2, BAD_PAGE = PIECE_BAD_PAGE, GAVE_UP = PIECE_GAVE_UP };
 
 template <typename T, int D, bool GATE, bool SHARED>
-__global__ void __launch_bounds__(NT, 1) decode_own_kernel(PagedStep a, PagedScratch s)
+__global__ void __launch_bounds__(OwnCfg<T, D>::NT, 1) decode_own_kernel(PagedStep a, PagedScratch s)
 {
     using C = OwnCfg<T, D>;
-    constexpr int LPR = C::LPR, RPP = C::RPP, GR = C::GR, CPL = C::CPL, S = C::STAGES;
+    constexpr int LPR = C::LPR, RPP = C::RPP, GR = C::GR, CPL = C::CPL, WARPS = C::WARPS, NT = C::NT;
     constexpr int VP = Vec<T>::N / 2;  // pairs of a chunk
     extern __shared__ __align__(128) char smem[];
     long long *s_cum = reinterpret_cast<long long *>(smem);  // before the rings are filled
-    __shared__ uint64_t s_bar[WARPS][S];
-    __shared__ long long s_row[WARPS][S];  // first row of the stage's granule in the pool, or -1
+    __shared__ uint64_t s_bar[WARPS][C::MORE_STAGES];
+    __shared__ long long s_row[WARPS][C::MORE_STAGES];  // first row of the stage's granule in the pool, or -1
     __shared__ Piece<D> s_piece[WARPS][2];
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int lr = lane % LPR, grp = lane / LPR;
@@ -177,7 +184,7 @@ __global__ void __launch_bounds__(NT, 1) decode_own_kernel(PagedStep a, PagedScr
 
     release_next();
     if (lane == 0) {
-        for (int i = 0; i < S; ++i) tc::mbar_init(&s_bar[warp][i], 1);
+        for (int i = 0; i < C::MORE_STAGES; ++i) tc::mbar_init(&s_bar[warp][i], 1);
         tc::mbar_fence_init();
         s_piece[warp][0].u = s_piece[warp][1].u = -1;
     }
@@ -191,11 +198,13 @@ __global__ void __launch_bounds__(NT, 1) decode_own_kernel(PagedStep a, PagedScr
     for (int b0 = 0; b0 < a.B; b0 += NT) {
         long long sum;
         mine = b0 + tid < a.B ? (long long)cost_of<GR>(c, b0 + tid) * a.H : 0;
-        at = block_scan(mine, &sum);
+        at = block_scan<WARPS>(mine, &sum);
         total += sum;
     }
-    const long long nw = min((long long)gridDim.x * WARPS, total);
-    const long long gw = (long long)blockIdx.x * WARPS + warp;
+    const bool few = WARPS > C::FEW && total >= (long long)gridDim.x * C::FEW * C::LONG_SHARE;
+    const int warps = few ? C::FEW : WARPS, S = few ? C::MORE_STAGES : C::STAGES;
+    const long long nw = min((long long)gridDim.x * warps, total);
+    const long long gw = warp < warps ? (long long)blockIdx.x * warps + warp : nw;
     const long long t0 = gw < nw ? total * gw / nw : total, t1 = gw < nw ? total * (gw + 1) / nw : total;
     Cursor cc{};
     long long cum = 0;
@@ -203,7 +212,7 @@ __global__ void __launch_bounds__(NT, 1) decode_own_kernel(PagedStep a, PagedScr
         long long sum = total;
         if (a.B > NT) {
             mine = b0 + tid < a.B ? (long long)cost_of<GR>(c, b0 + tid) * a.H : 0;
-            at = block_scan(mine, &sum);
+            at = block_scan<WARPS>(mine, &sum);
         }
         s_cum[tid] = cum + at;
         __syncthreads();
@@ -230,8 +239,8 @@ __global__ void __launch_bounds__(NT, 1) decode_own_kernel(PagedStep a, PagedScr
 
     if (cc.left > 0) {
         const float scale2 = a.scale * LOG2E;
-        char *ring = smem + warp * C::RING, *head = smem + WARPS * C::RING + warp * C::HEAD;
-        float *gring = reinterpret_cast<float *>(smem + WARPS * (C::RING + C::HEAD)) + warp * S * GR;
+        char *ring = smem + warp * S * 2 * C::TILE, *head = smem + C::SLOTS * 2 * C::TILE + warp * S * 2 * C::ROW;
+        float *gring = reinterpret_cast<float *>(smem + C::SLOTS * 2 * (C::TILE + C::ROW)) + warp * S * GR;
         T *K = static_cast<T *>(c.k), *Vp = static_cast<T *>(c.v);
 
         // The loads run ahead of the arithmetic by S granules, across units: a unit's first granule
@@ -648,7 +657,7 @@ template <typename T, int D, bool GATE, bool SHARED>
 cudaError_t run_own(const PagedStep &a, const PagedPlan &p, const PagedScratch &s, cudaStream_t st)
 {
     auto k = decode_own_kernel<T, D, GATE, SHARED>;
-    constexpr int smem = OwnCfg<T, D>::SMEM;
+    constexpr int smem = OwnCfg<T, D>::SMEM, NT = OwnCfg<T, D>::NT;
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     if (SHARED) return launch_overlapped(k, p.own_blocks, NT, smem, st, a, s);
@@ -685,7 +694,7 @@ PagedPlan paged_plan(int B, int H, int max_pages, int page, int d, int dt, int p
     const int sms = sm_count();
     const int gr = own_granule(d, (int)dtype_size(dt));
     const long long most = (long long)B * H * (((long long)max_pages * page - 1) / gr + 1);
-    const long long blocks = (most + WARPS - 1) / WARPS;
+    const long long blocks = (most + 7) / 8;  // eight warps or more
     p.own_blocks = (int)(blocks < sms ? blocks : sms);
     p.own_slots = p.own_blocks + B * H;
     // bf16: the prefix is read once for up to 64 queries, tiles of even size (their softmax is what

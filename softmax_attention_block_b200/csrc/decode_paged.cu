@@ -5,11 +5,17 @@
 //   row n <- k_new, v_new, g = 0;  out = softmax_j(scale q^T k_j + g_j) V.
 //
 // Bound by HBM: it reads K and V once and writes K once (3 d elements a row and
-// head) for about 8 d operations. Rows differ in length, so the (row, head)
-// units are cut into tiles of OWN_TILE rows and the list of all tiles is dealt
-// out to the blocks in equal contiguous shares (decode_own_kernel); pieces of a
-// unit meet in decode_join_kernel, in block order, so results repeat exactly.
-// The lengths are on the device: each block adds them up itself.
+// head) for about 8 d operations. 48 rows of 500 to 6000 tokens, 24 heads of 64,
+// bf16 with the gate: 249 us for 1475 MB, 5.9 TB/s (90% of a plain copy); 32 rows
+// of 1 to 8192, 32 heads of 128: 594 us for 3331 MB, 5.6 TB/s.
+//
+// Rows differ in length, so the (row, head) units are cut into granules of 16 rows
+// and the list of all granules is dealt out to the warps in equal contiguous shares
+// (decode_own_kernel). A warp keeps its loads in flight across units, as bulk copies
+// into a ring of its own: registers for loads in flight, as in the step over
+// contiguous caches, left one block an SM here and took 1.7 to 3.5 times as long.
+// Pieces of a unit meet in decode_join_kernel, in list order, so results repeat
+// exactly. The lengths are on the device: each block adds them up itself.
 #include "paged.cuh"
 #include "rowvec.cuh"
 #include "runtime.cuh"

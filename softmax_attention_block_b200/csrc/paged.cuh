@@ -46,7 +46,7 @@ __device__ __forceinline__ int length_of(const PagedCache &c, int slot)
     return n >= 0 && n < (long long)c.max_pages << c.page_log2 ? n : -1;
 }
 
-// Rows of a tile of the own part: 8 KB of keys and values, or 16 rows (the smallest page).
+// Rows of a granule of the own part: 8 KB of keys and values, or 16 rows (the smallest page).
 constexpr int own_granule(int d, int size) { return d * size == 512 ? 8 : 16; }
 
 // What went wrong with a piece (bits of own_flag and pre_flag)
@@ -58,8 +58,8 @@ constexpr int ERR_PAGE = 1000, ERR_PAGED_WAIT = 41;
 // Scratch of a step, carved from the caller's workspace.
 //
 // Both parts deal a list of tiles (units in order, a unit's tiles in order)
-// out to blocks in equal contiguous shares, so a unit may lie in several
-// blocks and a block may hold several units. The piece of unit u that block i
+// out to blocks in contiguous shares, so a unit may lie in several blocks and
+// a block may hold several units. The piece of unit u that block i
 // holds has the slot i + u: along the list i and u never fall and one of them
 // rises at every piece, so no two pieces share a slot.
 struct PagedScratch {

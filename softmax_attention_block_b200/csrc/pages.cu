@@ -266,7 +266,8 @@ __device__ __forceinline__ void copy_piece(const char *src, char *dst, int bytes
 
 // Pages of a move list: bound by HBM, each byte read and written once. Pieces of 32 KB keep
 // 8 loads of a thread in flight (16 KB pieces: 4% slower; bulk copies through shared memory:
-// within 2% of these).
+// within 2% of these). 32 sequences of 200 to 1500 tokens, 32 heads of 128: 151 us for 946 MB,
+// 6.3 TB/s.
 __global__ void __launch_bounds__(COPY_THREADS) copy_kernel(PagesCopy a)
 {
     const int n = min(a.info[1], a.max_moves);
@@ -297,7 +298,8 @@ __global__ void __launch_bounds__(COPY_THREADS) copy_kernel(PagesCopy a)
 }
 
 // One page of one head at a time: its rows are contiguous on both sides. Its keys and values
-// are loaded together; what is read once is not kept in the caches.
+// are loaded together; what is read once is not kept in the caches. 8 x 24 heads of 64, 1 to
+// 4096 tokens: 40 us for 217 MB, 5.4 TB/s (47 us one after the other and without the hints).
 __global__ void __launch_bounds__(COPY_THREADS) store_kernel(PagesStore a)
 {
     constexpr int VECS = 2, PIECE = COPY_THREADS * VECS * 16;
@@ -342,6 +344,7 @@ __global__ void __launch_bounds__(COPY_THREADS) store_kernel(PagesStore a)
     }
 }
 
+// 32 x 32 heads of 128: 21 us for 134 MB (6.3 TB/s).
 __global__ void __launch_bounds__(256) state_copy_kernel(float *state, float *g_state, const int *parents,
                                                          const int *children, int n_slots, int H, int d)
 {

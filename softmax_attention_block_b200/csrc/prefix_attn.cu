@@ -22,6 +22,7 @@ constexpr float LOG2E = 1.4426950408889634f;
 // One (batch row, head): G read once and written once, bound by HBM (8 d^2
 // bytes). A thread keeps D * D / 512 vectors of four columns in registers, so that a
 // block's whole G is on its way at once, and only four partial sums of a column meet.
+// 32 x 32 heads of 128: 21 us for 134 MB (6.3 TB/s), 27 us with 256 threads a block.
 constexpr int TT = 128;
 
 template <typename T, int D>
@@ -150,7 +151,8 @@ __global__ void __launch_bounds__(TT) turn_kernel(PagedStep a, PagedScratch s, i
 // for 16 of outputs), or for few tiles by their latency. Where a key's row
 // lies is looked up a tile ahead, so that the asynchronous copies of a tile wait
 // for nothing; a tile's keys come in under the former tile's values, its values
-// under its own keys.
+// under its own keys. A step of 9 rows behind 2047 tokens (6 heads of 128), where a
+// block has one tile: 26 us with 16 queries a tile, 33 with 32.
 constexpr int KT = 64;
 
 template <int D, int QT>

@@ -7,7 +7,7 @@
 // Bound by HBM: it reads K and V once and writes K once (3 d elements a row and
 // head) for about 8 d operations. 48 rows of 500 to 6000 tokens, 24 heads of 64,
 // bf16 with the gate: 249 us for 1475 MB, 5.9 TB/s (90% of a plain copy); 32 rows
-// of 1 to 8192, 32 heads of 128: 594 us for 3331 MB, 5.6 TB/s.
+// of 1 to 8192, 32 heads of 128: 579 us for 3331 MB, 5.8 TB/s (88%).
 //
 // Rows differ in length, so the (row, head) units are cut into granules of 16 rows
 // and the list of all granules is dealt out to the warps in equal contiguous shares
@@ -254,6 +254,11 @@ __global__ void __launch_bounds__(OwnCfg<T, D>::NT, 1) decode_own_kernel(PagedSt
         // token, which lands in the tile at its row.
         Cursor pc = cc;
         int tab_b = -1, tab_at = 0, tab = -1;  // 32 entries of row tab_b's table, one a lane
+        // Values are not touched again before the next step; letting go of them first leaves L2 to the
+        // keys on their way back (32 rows of 1 to 8192, 32 heads of 128: 594 -> 579 us). With rows of
+        // 128 bytes (253 -> 256) or behind a prefix (154 -> 156) the hint costs more than it gives.
+        constexpr bool HINT = C::ROW > 128 && !SHARED;
+        const uint64_t once = HINT ? tc::l2_evict_first() : 0;
         bool begun = false;
         float p_beta = 0.f, p_lf = 0.f;
         auto load = [&](int st) {
@@ -292,7 +297,10 @@ __global__ void __launch_bounds__(OwnCfg<T, D>::NT, 1) decode_own_kernel(PagedSt
                 if (ok) {
                     if (bytes) {
                         tc::bulk_load(tk, K + row * D, bytes, bar);
-                        tc::bulk_load(tv, Vp + row * D, bytes, bar);
+                        if (HINT)
+                            tc::bulk_load(tv, Vp + row * D, bytes, bar, once);
+                        else
+                            tc::bulk_load(tv, Vp + row * D, bytes, bar);
                     }
                     if (fresh) {
                         tc::bulk_load(tk + bytes, static_cast<const T *>(a.k_new) + pu * D, C::ROW, bar);

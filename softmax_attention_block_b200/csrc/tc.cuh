@@ -233,17 +233,6 @@ __device__ __forceinline__ void tmem_wait_ld_tied(float (&a)[16], float (&b)[16]
                  : "memory");
 }
 
-// The same for one set of registers.
-__device__ __forceinline__ void tmem_wait_ld_tied(float (&a)[16])
-{
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+f"(a[0]), "+f"(a[1]), "+f"(a[2]), "+f"(a[3]), "+f"(a[4]), "+f"(a[5]),
-                   "+f"(a[6]), "+f"(a[7]), "+f"(a[8]), "+f"(a[9]), "+f"(a[10]), "+f"(a[11]),
-                   "+f"(a[12]), "+f"(a[13]), "+f"(a[14]), "+f"(a[15])
-                 :
-                 : "memory");
-}
-
 // --- mbarriers --------------------------------------------------------------
 __device__ __forceinline__ void mbar_init(uint64_t *bar, uint32_t count)
 {

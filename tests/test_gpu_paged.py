@@ -245,6 +245,7 @@ PREFIX = [
     (300, [2] * 130, 1, 256, True),
     (2500, [3, 0], 1, 1024, False),
     (77, [i % 5 for i in range(600)], 1, 16, False),
+    (6000, [1] * 20, 30, 16, True),
 ]
 
 
@@ -285,6 +286,23 @@ def test_lowest_values_infinities_and_nan(P, prefix):
     out = c.call(P, x)
     assert torch.equal(out[:, 0], x["v_new"][:, 0])
     assert torch.isnan(out[0, 2]).all() and torch.isfinite(out[1]).all() and torch.isfinite(out[0, :2]).all()
+
+
+@pytest.mark.parametrize("prefix", [0, 40])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_a_batch_of_idle_rows(P, prefix, dtype):
+    """Nothing is written, and the call after it is as ever."""
+    c = Cache([20, 33], 2, 64, 16, dtype, True, prefix=prefix)
+    before, x = c.snap(), c.step_inputs()
+    out = torch.full_like(x["q"], 5.0)
+    ws = torch.full((P.path_decode_paged_workspace_bytes(2, 2, c.M, 16, 64, dtype, prefix),), 0xFF,
+                    dtype=torch.uint8, device="cuda")
+    c.call(P, x, out=out, workspace=ws, rows=ints([-1, -7]))
+    assert (out == 5.0).all() and P.path_attn_wait_status(ws) == 0
+    for a, b in zip(before, c.snap()):
+        assert a is None or torch.equal(torch.nan_to_num(a.float()), torch.nan_to_num(b.float()))
+    c.call(P, x, out=out, workspace=ws)
+    c.check(before, x, out)
 
 
 @pytest.mark.parametrize("prefix", [0, 200])

@@ -342,8 +342,8 @@ path_status path_decode_step_paged(const void *q, const void *k_new, const void 
  * The own rows, lens, errors and everything else as path_decode_step_paged; an
  * out-of-range page of the prefix makes every row NaN. The prefix's pages must not be
  * among the pages of the batch's slots. PATH_BF16: queries turned back and weights meet the
- * prefix on the tensor cores as sums of two bf16 numbers (off by 2^-17), so an infinite key
- * or value of the prefix may turn into NaN.
+ * prefix on the tensor cores as sums of three bf16 numbers, which hold fp32's 24 bits; an
+ * infinite key or value of the prefix may turn into NaN, where the parts have both signs.
  */
 path_status path_decode_step_shared(const void *q, const void *k_new, const void *v_new, const void *w,
                                     const float *beta, const float *log_f, float scale, int B, int H,

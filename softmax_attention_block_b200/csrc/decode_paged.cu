@@ -711,9 +711,9 @@ PagedPlan paged_plan(int B, int H, int max_pages, int page, int d, int dt, int p
     const long long blocks = (most + 7) / 8;  // eight warps or more
     p.own_blocks = (int)(blocks < sms ? blocks : sms);
     p.own_slots = p.own_blocks + B * H;
-    // bf16: the prefix is read once for up to 64 queries, tiles of even size (their softmax is what
-    // can take longer than the loads); fp32: tiles of the CUDA-core kernel
-    p.q_tile = dt == BF16 ? ceil_div(ceil_div(B, ceil_div(B, 64)), 16) * 16 : B <= 16 ? 16 : 32;
+    // bf16: the prefix is read once for up to 64 queries (48 at d = 128: shared memory), tiles of even
+    // size (their softmax is what can take longer than the loads); fp32: tiles of the CUDA-core kernel
+    p.q_tile = dt == BF16 ? ceil_div(ceil_div(B, ceil_div(B, d == 64 ? 64 : 48)), 16) * 16 : B <= 16 ? 16 : 32;
     p.q_tiles = ceil_div(B, p.q_tile);
     p.key_tile = dt == BF16 ? 128 : 64;
     p.key_tiles = (int)(((long long)prefix_len + p.key_tile - 1) / p.key_tile);
@@ -734,7 +734,7 @@ size_t paged_carve(void *base, const PagedPlan &p, int B, int H, int d, PagedScr
     s.last = c.take<int>(nh);
     s.own = c.take<float>(own * (d + 2));
     s.own_flag = c.take<int>(own);
-    s.qt = c.take<float>((size_t)p.q_tiles * p.q_tile * H * d);
+    s.qt = reinterpret_cast<float *>(c.take<bf16>(PREFIX_PARTS * (size_t)p.q_tiles * p.q_tile * H * d));  // fp32: less
     s.qg = c.take<float>((size_t)p.q_tiles * p.q_tile * H);
     // room for the largest tile, so that a larger batch never needs less
     s.pre = c.take<float>(pre * 64 * d);

@@ -49,6 +49,9 @@ __device__ __forceinline__ int length_of(const PagedCache &c, int slot)
 // Rows of a granule of the own part: 8 KB of keys and values, or 16 rows (the smallest page).
 constexpr int own_granule(int d, int size) { return d * size == 512 ? 8 : 16; }
 
+// bf16 numbers whose sum is an fp32 number: 3 x 8 bits and more (a sum of two is off by 2^-17).
+constexpr int PREFIX_PARTS = 3;
+
 // What went wrong with a piece (bits of own_flag and pre_flag)
 enum { PIECE_BAD_PAGE = 4, PIECE_GAVE_UP = 8 };
 
@@ -68,7 +71,7 @@ struct PagedScratch {
     float *own;        // [own_slots, d + 2]: max (log2 domain), sum, accumulator
     int *own_flag;     // [own_slots] bits 2, 3: see PIECE_*
     // the queries turned back to the prefix's end, q_rows = q_tiles * q_tile of a head (zero past
-    // the batch): [H, q_rows, d] fp32, or for the tensor cores [2, H, q_rows, d] bf16, hi and lo
+    // the batch): [H, q_rows, d] fp32, or for the tensor cores [PREFIX_PARTS, H, q_rows, d] bf16
     float *qt;
     float *qg;         // [H, q_rows] the gate's bias since the prefix's end (log2 domain)
     float *pre;        // [pre_slots, q_tile, d] accumulators of the prefix part

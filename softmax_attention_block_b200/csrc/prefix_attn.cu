@@ -39,14 +39,14 @@ __global__ void __launch_bounds__(TT) turn_kernel(PagedStep a, PagedScratch s, i
     const int slot = b < a.B ? slot_of(a.c, b) : -1;
     const long long row = (long long)h * q_rows + b;
     float4 *qt = reinterpret_cast<float4 *>(s.qt) + row * CG;  // fp32
-    uint2 *qhi = reinterpret_cast<uint2 *>(s.qt) + row * CG;   // bf16, hi and lo
-    uint2 *qlo = qhi + (long long)a.H * q_rows * CG;
+    uint2 *qb = reinterpret_cast<uint2 *>(s.qt) + row * CG;    // bf16, its parts one after the other
+    const long long part = (long long)a.H * q_rows * CG;
     if (slot < 0 || length_of(a.c, slot) < 0) {  // past the batch, idle or invalid: a query of zeros
         if (tid < CG) {
             if (sizeof(T) == 4)
                 qt[tid] = make_float4(0.f, 0.f, 0.f, 0.f);
             else
-                qhi[tid] = qlo[tid] = make_uint2(0u, 0u);
+                for (int i = 0; i < PREFIX_PARTS; ++i) qb[i * part + tid] = make_uint2(0u, 0u);
         }
         if (tid == 0) s.qg[row] = 0.f;
         return;
@@ -120,17 +120,20 @@ __global__ void __launch_bounds__(TT) turn_kernel(PagedStep a, PagedScratch s, i
         const float4 r = make_float4(fmaf(f, y.x, z.x), fmaf(f, y.y, z.y), fmaf(f, y.z, z.z), fmaf(f, y.w, z.w));
         if (sizeof(T) == 4) {
             qt[cg] = r;
-        } else {  // r = hi + lo to 2^-17
-            const float v[4] = {r.x, r.y, r.z, r.w};
-            __nv_bfloat162 hi[2], lo[2];
+        } else {  // r as a sum of bf16 numbers
+            float v[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                hi[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-                const float2 t = __bfloat1622float2(hi[i]);
-                lo[i] = __floats2bfloat162_rn(v[2 * i] - t.x, v[2 * i + 1] - t.y);
+            for (int j = 0; j < PREFIX_PARTS; ++j) {
+                __nv_bfloat162 b[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    b[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+                    const float2 t = __bfloat1622float2(b[i]);
+                    v[2 * i] -= t.x;
+                    v[2 * i + 1] -= t.y;
+                }
+                qb[j * part + cg] = *reinterpret_cast<uint2 *>(b);
             }
-            qhi[cg] = *reinterpret_cast<uint2 *>(hi);
-            qlo[cg] = *reinterpret_cast<uint2 *>(lo);
         }
     }
     if (tid == 0) {

@@ -11,12 +11,11 @@
 // queries no lane idles (queries along the lanes would leave 3 of 4 empty at 32).
 // Both products come out in the layout that the next step reads.
 //
-// bf16 operands alone would cost as much accuracy as the rounding of the output,
-// so qt and P are each split in two bf16 numbers (hi + lo, off by 2^-17). The tensor
-// cores have the time: a product of 16 keys or dims takes about 75 cycles whatever its
-// other sides are, a tile D / 8 of them for S^T (hi and lo one after the other) and 8
-// for O^T (hi | lo side by side), 1200 at D = 64 and 1800 at 128, where its loads take
-// 1400 and 2800.
+// bf16 operands alone would cost as much accuracy as the rounding of the output, and sums
+// of two bf16 numbers (off by 2^-17) still show in the outputs' last bits. So qt and P are
+// each split in three (hi + mid + lo), which hold an fp32 number's 24 bits: nothing of either
+// is rounded. The products are S^T's D / 16 steps for each part, one part after the other, and
+// 8 steps for O^T with the parts side by side as columns.
 //
 // The running maximum of a query is a reference that moves only when a logit
 // passes it by more than 2^8 (or at a unit's first tile): then the warps that
@@ -49,27 +48,30 @@ using namespace tc;
 
 constexpr int KT = 128;
 constexpr int CN = 16;  // queries of a softmax group
+constexpr int PARTS = PREFIX_PARTS;  // bf16 numbers that make an fp32 one
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LOW = -1e30f;  // reference of a query that has no weight yet
 constexpr float SLACK = 8.f;
 
-// GROUPS softmax groups: units of QT = 16 GROUPS queries. QN is the room for them.
+// GROUPS softmax groups: units of QT = 16 GROUPS queries, QN the distance of the two S^T.
 template <int D, int GROUPS>
 struct Cfg {
     static constexpr int PANELS = D / 64, QT = CN * GROUPS, QN = QT <= 32 ? 32 : 64;
     static constexpr int W_LOAD = 4 * GROUPS, W_S = W_LOAD + 1, W_O = W_S + 1, NT = 32 * (W_O + 1);
     static constexpr int TILE = KT * D * 2;             // one operand tile
-    static constexpr int NK = D == 64 ? 4 : QN == 32 ? 3 : 2, NV = D == 64 ? 4 : 2, NG = NV + 1;
-    static constexpr int Q = 2 * QN * D * 2;            // hi and lo
+    static constexpr int Q = PARTS * QT * D * 2;        // hi, mid, lo
     static constexpr int PP = KT * 128;                 // one panel of P: 64 columns
-    static constexpr int P = QN == 32 ? PP : 2 * PP;    // hi | lo side by side, or a panel each
-    static constexpr int NP = D == 128 && QN == 64 ? 1 : 2;  // buffers of P
+    static constexpr int P_PANELS = (PARTS * QT + 63) / 64, P = P_PANELS * PP;  // hi | mid | lo side by side
+    static constexpr int NP = D == 128 && QT > 32 ? 1 : 2;  // buffers of P
+    // buffers of keys and values: what is left
+    static constexpr int NK = D == 64 ? P_PANELS == 3 ? 3 : 4 : QT == 16 ? 3 : 2, NV = D == 64 ? NK : 2, NG = NV + 1;
     static constexpr int K_OFF = 0, V_OFF = K_OFF + NK * TILE, Q_OFF = V_OFF + NV * TILE, P_OFF = Q_OFF + Q;
     static constexpr int G_OFF = P_OFF + NP * P, M_OFF = G_OFF + NG * KT * 4, F_OFF = M_OFF + QN * 4;
     static constexpr int RED_OFF = F_OFF + QN * 4, BAR_OFF = RED_OFF + 4 * QN * 4;
     static constexpr int NBAR = 2 * NK + 2 * NV + 9;
     static constexpr int SMEM = BAR_OFF + NBAR * 8 + 16 + 1024;
-    static constexpr int T_S = 0, T_O = 2 * QN, TMEM = 4 * QN;  // two S^T, then O^T for hi | lo
+    static constexpr int T_S = 0, T_O = 2 * QN, T_END = T_O + PARTS * QT;  // two S^T, then O^T for hi | mid | lo
+    static constexpr int TMEM = T_END <= 128 ? 128 : T_END <= 256 ? 256 : 512;
     static_assert(SMEM <= 232448, "shared memory");
 };
 
@@ -194,12 +196,10 @@ __global__ void __launch_bounds__(Cfg<D, GROUPS>::NT, 1)
                 }
                 if (seg == 0) wait_previous();  // the queries; keys and values are nobody's output
                 if (lane == 0) {
-                    mbar_expect_tx(q_full, 2 * QT * D * 2);
+                    mbar_expect_tx(q_full, C::Q);
                     const int row = h * q_rows + qt * QT;
-                    for (int x = 0; x < PANELS; ++x) {
-                        tma_load_2d(sm + C::Q_OFF + x * QN * 128, &mQ, 64 * x, row, q_full);
-                        tma_load_2d(sm + C::Q_OFF + (PANELS + x) * QN * 128, &mQ, 64 * x, a.H * q_rows + row, q_full);
-                    }
+                    for (int x = 0; x < PARTS * PANELS; ++x)
+                        tma_load_2d(sm + C::Q_OFF + x * QT * 128, &mQ, 64 * (x % PANELS), x / PANELS * a.H * q_rows + row, q_full);
                 }
                 ++seg;
             }
@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(Cfg<D, GROUPS>::NT, 1)
             if (seg > 0) mbar_wait(q_full, (seg - 1) & 1, WAIT_LIMIT_NS);
         }
     } else if (warp == W_S) {
-        // S^T = K . qt^T, hi then lo. The whole warp runs along, converged, and one lane issues:
+        // S^T = K . qt^T, hi, mid, lo. The whole warp runs along, converged, and one lane issues:
         // descriptors stay uniform, and differ from a base by the address in their low bits.
         const uint32_t issue = lane == 0;
         constexpr uint32_t id = idesc_f16(128, QT, AB_BF16, 0, 0);
@@ -273,11 +273,11 @@ __global__ void __launch_bounds__(Cfg<D, GROUPS>::NT, 1)
             const uint64_t kd = k0 + ks * (C::TILE >> 4);
             const uint32_t d = tbase + C::T_S + (n & 1) * QN;
 #pragma unroll
-            for (int part = 0; part < 2; ++part)
+            for (int part = 0; part < PARTS; ++part)
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
                     mma_ss_if(issue, d, kd + (((kk / 4) * KT * 128 + (kk % 4) * 32) >> 4),
-                              q0 + (((part * PANELS + kk / 4) * QN * 128 + (kk % 4) * 32) >> 4), id, part + kk > 0);
+                              q0 + (((part * PANELS + kk / 4) * QT * 128 + (kk % 4) * 32) >> 4), id, part + kk > 0);
             commit_if(issue, &s_full[n & 1]);
             commit_if(issue, &k_empty[ks]);
             if (++kt == p.key_tiles) kt = 0;
@@ -294,9 +294,9 @@ __global__ void __launch_bounds__(Cfg<D, GROUPS>::NT, 1)
         commit_if(issue, mma_done);
         mbar_wait(mma_done, 0, 8 * WAIT_LIMIT_NS);
     } else if (warp == W_O) {
-        // O^T += V^T . P, hi | lo as columns
+        // O^T += V^T . P, hi | mid | lo as columns
         const uint32_t issue = lane == 0;
-        constexpr uint32_t id = idesc_f16(D, QN + QT, AB_BF16, 1, 1);
+        constexpr uint32_t id = idesc_f16(D, PARTS * QT, AB_BF16, 1, 1);
         const uint64_t v0 = desc_sw128(smem_u32(sm + C::V_OFF), KT * 128, 1024), p0 = desc_sw128(smem_u32(sm + C::P_OFF), C::PP, 1024);
         int kt = (int)(t0 % p.key_tiles);
         bool ok = true;
@@ -331,9 +331,14 @@ __global__ void __launch_bounds__(Cfg<D, GROUPS>::NT, 1)
             __syncwarp();
         };
         auto product_done = [&](int i) { wait(&o_done[i & 1], (i >> 1) & 1); };
-        // this thread's row of P: chunk j of eight queries, hi and lo
-        const uint32_t hi0 = sw128_offset(gt, c0), hi1 = sw128_offset(gt, c0 + 8);
-        const uint32_t lo0 = QN == 32 ? sw128_offset(gt, 32 + c0) : C::PP + hi0, lo1 = QN == 32 ? sw128_offset(gt, 40 + c0) : C::PP + hi1;
+        // this thread's row of P: where each part's first chunk of eight queries lies (the second is
+        // its neighbour, 16 bytes off in one direction or the other)
+        uint32_t p_at[PARTS];
+#pragma unroll
+        for (int part = 0; part < PARTS; ++part) {
+            const int col = part * QT + c0;
+            p_at[part] = col / 64 * C::PP + sw128_offset(gt, col % 64);
+        }
         uint32_t gslot = 0;
         int n = 0, u = (int)(t0 / p.key_tiles), kb = (int)(t0 % p.key_tiles);
         int h = u / p.q_tiles, qt = u % p.q_tiles;
@@ -400,8 +405,8 @@ __global__ void __launch_bounds__(Cfg<D, GROUPS>::NT, 1)
 #pragma unroll
                         for (int i = 0; i < CN; ++i) l[i] *= sF[c0 + i];
 #pragma unroll 1
-                        for (int part = 0; part < 2; ++part) {  // hi, lo
-                            const uint32_t at = tbase + C::T_O + part * QN + c0 + lane_off;
+                        for (int part = 0; part < PARTS; ++part) {
+                            const uint32_t at = tbase + C::T_O + part * QT + c0 + lane_off;
                             float o[CN];
                             tmem_ld16_wait(at, o);
 #pragma unroll
@@ -417,22 +422,28 @@ __global__ void __launch_bounds__(Cfg<D, GROUPS>::NT, 1)
                     logits();
                     minus_ref();
                 }
-                // weights, split in two bf16 numbers; this thread's key is a row of P
+                // weights, split in three bf16 numbers; this thread's key is a row of P
                 uint8_t *sP = sm + C::P_OFF + (n % NP) * C::P;
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    uint32_t hi[4], lo[4];
+                    uint32_t w[PARTS][4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int i = 8 * j + 2 * e;
-                        const float x = ex2(z[i]), y = ex2(z[i + 1]);
+                        float x = ex2(z[i]), y = ex2(z[i + 1]);
                         l[i] += x;
                         l[i + 1] += y;
-                        hi[e] = pack_bf16(x, y);
-                        lo[e] = pack_bf16(x - __uint_as_float(hi[e] << 16), y - __uint_as_float(hi[e] & 0xffff0000u));
+#pragma unroll
+                        for (int part = 0; part < PARTS; ++part) {
+                            w[part][e] = pack_bf16(x, y);
+                            x -= __uint_as_float(w[part][e] << 16);
+                            y -= __uint_as_float(w[part][e] & 0xffff0000u);
+                        }
                     }
-                    *reinterpret_cast<uint4 *>(sP + (j ? hi1 : hi0)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4 *>(sP + (j ? lo1 : lo0)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+#pragma unroll
+                    for (int part = 0; part < PARTS; ++part)
+                        *reinterpret_cast<uint4 *>(sP + (p_at[part] ^ (16 * j))) =
+                            make_uint4(w[part][0], w[part][1], w[part][2], w[part][3]);
                 }
                 // values behind the prefix's end are whatever the page holds, and are weighed with
                 // zero: make them zero too
@@ -459,12 +470,17 @@ __global__ void __launch_bounds__(Cfg<D, GROUPS>::NT, 1)
             {
                 const int dim = D == 128 ? gt : 16 * (warp % 4) + lane;
                 float v[CN], v2[CN];
-                tmem_ld16_wait(tbase + C::T_O + c0 + lane_off, v);
-                tmem_ld16_wait(tbase + C::T_O + QN + c0 + lane_off, v2);
+                tmem_ld16_wait(tbase + C::T_O + (PARTS - 1) * QT + c0 + lane_off, v);  // the small parts first
+#pragma unroll
+                for (int part = PARTS - 2; part >= 0; --part) {
+                    tmem_ld16_wait(tbase + C::T_O + part * QT + c0 + lane_off, v2);
+#pragma unroll
+                    for (int i = 0; i < CN; ++i) v[i] += v2[i];
+                }
                 if (D == 128 || lane < 16) {
 #pragma unroll
                     for (int i = 0; i < CN; ++i)
-                        if (i < nq) s.pre[(piece * QT + c0 + i) * D + dim] = v[i] + v2[i];
+                        if (i < nq) s.pre[(piece * QT + c0 + i) * D + dim] = v[i];
                 }
 #pragma unroll
                 for (int i = 0; i < CN; ++i) v[i] = l[i];
@@ -505,7 +521,7 @@ cudaError_t run(const PagedStep &a, const PagedPlan &p, const PagedScratch &s, c
     const int page = 1 << a.c.page_log2;
     const uint64_t rows = (uint64_t)a.c.n_pages * a.H * page;
     CUtensorMap mQ, mK, mV;
-    if (!make_map_2d(&mQ, s.qt, BF16, D, 2ull * a.H * p.q_tiles * p.q_tile, p.q_tile) ||
+    if (!make_map_2d(&mQ, s.qt, BF16, D, (uint64_t)PARTS * a.H * p.q_tiles * p.q_tile, p.q_tile) ||
         !make_map_2d(&mK, a.c.k, BF16, D, rows, page < KT ? page : KT) ||
         !make_map_2d(&mV, a.c.v, BF16, D, rows, page < KT ? page : KT))
         return cudaErrorInvalidValue;
@@ -522,7 +538,9 @@ cudaError_t run(const PagedStep &a, const PagedPlan &p, const PagedScratch &s, c
     case 1: return run<D, 1>(a, p, s, st);
     case 2: return run<D, 2>(a, p, s, st);
     case 3: return run<D, 3>(a, p, s, st);
-    default: return run<D, 4>(a, p, s, st);
+    default:
+        if constexpr (D == 64) return run<D, 4>(a, p, s, st);
+        return cudaErrorInvalidValue;
     }
 }
 

@@ -1,0 +1,73 @@
+"""The paged decode cache on the GPU where it can go wrong: precision behind a prefix, layouts that
+only large batches take, error paths, padded prefills. Plain 64-bit arithmetic is the reference;
+each tolerance is derived where it stands."""
+import math
+
+import pytest
+import torch
+
+from test_gpu_paged import BF, F32, Cache, P, ints  # noqa: F401 (P: the fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("B,gate", [(7, True), (20, False), (40, True), (64, False)])
+def test_queries_and_weights_meet_the_prefix_in_fp32(P, B, gate, dtype, d):
+    """The turned-back query and the softmax weights are fp32 numbers, whatever the type of the
+    cache. Values of three keys of a prefix are chosen so that their weighted sum all but vanishes
+    in dim b of row b: what is left is the error of the weights, not the rounding of the output.
+
+    w = 0 leaves the state as it is, and one-hot queries and keys make a logit one product
+    z = scale G[r, i] c without a sum, G[r, i] being any fp32 number. In log2 units that
+    logit is off by 6 steps of 2^-24 relative (two accumulations of parts of G, each cut or rounded
+    to 24 bits: 2^-23 each; log2 e, the product and the sum with the gate: 2^-24 each, and 2^-24 in
+    reserve), its gate bias by 4 (two products, two sums) and the maxima it is taken against by 4
+    (a difference in the tile, one in the join, twice rounded); the exponentials of
+    the weight and of the join, with their products, are off by 2^-20 in all."""
+    H, page, n, J = 3, 16, 200, (5, 130, 199)
+    c = Cache([0] * B, H, d, page, dtype, gate, seed=B + d, prefix=n)
+    rng = torch.Generator(device="cuda").manual_seed(B)
+    c.state = torch.randn(c.state.shape, device="cuda", generator=rng)
+    x = c.step_inputs()
+    for name in ("w", "v_new", "k_new", "q"):
+        x[name].zero_()
+    r = torch.randint(d, (B, H), device="cuda", generator=rng)
+    x["q"].scatter_(2, r.unsqueeze(2), 1.0)
+    i, size = [3, 17, 50], [1.75, -2.0, 1.5]
+    pre, g = c.pages(None), torch.zeros((H, n), dtype=torch.float64, device="cuda")
+    for p in pre:
+        c.k[p] = 0
+        c.v[p] = 0
+    for j, key in enumerate(J):
+        c.k[pre[key // page], :, key % page, i[j]] = size[j]
+    if gate:
+        g = c.rows(c.g, None, n)
+    S = c.state[c.slot].double().gather(2, r[:, :, None, None].expand(B, H, 1, d)).squeeze(2)  # row r
+    z = g.unsqueeze(0).repeat(B, 1, 1)
+    for j, key in enumerate(J):
+        z[:, :, key] += S[:, :, i[j]] * size[j]
+    a, at = z[:, :, list(J)].exp().sort(-1, descending=True)  # weights, and which key each is of
+    bf = lambda t: t.to(BF).double()
+    v = torch.ones_like(a)
+    v[..., 0] = -bf(a[..., 1] / a[..., 0])
+    v[..., 2] = -bf((a * v)[..., :2].sum(-1) / a[..., 2])
+    v = torch.empty_like(v).scatter_(-1, at, v)
+    for j, key in enumerate(J):
+        for b in range(B):
+            c.v[pre[key // page], :, key % page, b] = v[b, :, j].to(dtype)
+    out = c.call(P, x, scale=1.0)
+    gs = c.gs[c.slot].double().unsqueeze(-1) if gate else 0.0  # after the step
+    weights = (z + gs).exp()
+    total = weights.sum(-1) + 1.0  # and the new token's
+    parts = weights[:, :, list(J)] * v
+    ref = parts.sum(-1) / total
+    l2e = math.log2(math.e)
+    zl, gl = (z - g).abs().amax(-1) * l2e, (g.abs().amax(-1) + (gs.abs().squeeze(-1) if gate else 0.0)) * l2e
+    eps = math.log(2) * 2.0 ** -23 * (6 * zl + 4 * gl + 4 * (zl + gl)) + 2.0 ** -20
+    tol = parts.abs().sum(-1) / total * eps + 2.0 ** -8 * ref.abs()
+    dim = torch.arange(B, device="cuda")
+    err = (out.double()[dim, :, dim] - ref).abs()
+    worst = (err / tol).max().item()
+    assert worst <= 1, f"off by {worst} of what fp32 weights and queries may be"

@@ -14,12 +14,17 @@
 // bf16 operands alone would cost as much accuracy as the rounding of the output, and sums
 // of two bf16 numbers (off by 2^-17) still show in the outputs' last bits. So qt and P are
 // each split in three (hi + mid + lo), which hold an fp32 number's 24 bits: nothing of either
-// is rounded. The products are S^T's D / 16 steps for each part, one part after the other, and
+// is rounded. The products are S^T's D / 16 steps for each part, the small parts first, and
 // 8 steps for O^T with the parts side by side as columns.
+//
+// A step cuts the sum so far to 24 bits instead of rounding it, so a long O^T would drift towards
+// zero (832 steps: by 3.4e-5 of the weights' sum). Every 8 tiles the softmax warps therefore add its
+// parts to a total in tensor memory, in rounded fp32, and start them from zero (0.8e-6; 121 -> 123 us
+// for the step of 96 x 24 heads of 64 below, every 4 tiles 126 us; 156 -> 157 us at 32 x 32 of 128).
 //
 // The running maximum of a query is a reference that moves only when a logit
 // passes it by more than 2^8 (or at a unit's first tile): then the warps that
-// hold the query agree on the new one and O^T is scaled in tensor memory. Otherwise a tile
+// hold the query agree on the new one and O^T joins its total, scaled. Otherwise a tile
 // needs no maximum across threads at all: weights stay below 2^8 and sums and
 // products are fp32. A thread keeps the sum of its own keys' weights per query;
 // they are added up across threads at a unit's end.
@@ -52,6 +57,7 @@ constexpr int PARTS = PREFIX_PARTS;  // bf16 numbers that make an fp32 one
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LOW = -1e30f;  // reference of a query that has no weight yet
 constexpr float SLACK = 8.f;
+constexpr int FOLD = 8;  // tiles after which O^T's parts are added to its total
 
 // GROUPS softmax groups: units of QT = 16 GROUPS queries, QN the distance of the two S^T.
 template <int D, int GROUPS>
@@ -70,7 +76,7 @@ struct Cfg {
     static constexpr int RED_OFF = F_OFF + QN * 4, BAR_OFF = RED_OFF + 4 * QN * 4;
     static constexpr int NBAR = 2 * NK + 2 * NV + 9;
     static constexpr int SMEM = BAR_OFF + NBAR * 8 + 16 + 1024;
-    static constexpr int T_S = 0, T_O = 2 * QN, T_END = T_O + PARTS * QT;  // two S^T, then O^T for hi | mid | lo
+    static constexpr int T_S = 0, T_O = 2 * QN, T_T = T_O + PARTS * QT, T_END = T_T + QT;  // two S^T, O^T for hi | mid | lo, its total
     static constexpr int TMEM = T_END <= 128 ? 128 : T_END <= 256 ? 256 : 512;
     static_assert(SMEM <= 232448, "shared memory");
 };
@@ -254,7 +260,7 @@ __global__ void __launch_bounds__(Cfg<D, GROUPS>::NT, 1)
             if (seg > 0) mbar_wait(q_full, (seg - 1) & 1, WAIT_LIMIT_NS);
         }
     } else if (warp == W_S) {
-        // S^T = K . qt^T, hi, mid, lo. The whole warp runs along, converged, and one lane issues:
+        // S^T = K . qt^T, lo, mid, hi: the sum that a step cuts is small until hi comes. The whole warp runs along, converged, and one lane issues:
         // descriptors stay uniform, and differ from a base by the address in their low bits.
         const uint32_t issue = lane == 0;
         constexpr uint32_t id = idesc_f16(128, QT, AB_BF16, 0, 0);
@@ -273,11 +279,11 @@ __global__ void __launch_bounds__(Cfg<D, GROUPS>::NT, 1)
             const uint64_t kd = k0 + ks * (C::TILE >> 4);
             const uint32_t d = tbase + C::T_S + (n & 1) * QN;
 #pragma unroll
-            for (int part = 0; part < PARTS; ++part)
+            for (int part = PARTS - 1; part >= 0; --part)
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
                     mma_ss_if(issue, d, kd + (((kk / 4) * KT * 128 + (kk % 4) * 32) >> 4),
-                              q0 + (((part * PANELS + kk / 4) * QT * 128 + (kk % 4) * 32) >> 4), id, part + kk > 0);
+                              q0 + (((part * PANELS + kk / 4) * QT * 128 + (kk % 4) * 32) >> 4), id, part < PARTS - 1 || kk > 0);
             commit_if(issue, &s_full[n & 1]);
             commit_if(issue, &k_empty[ks]);
             if (++kt == p.key_tiles) kt = 0;
@@ -346,8 +352,19 @@ __global__ void __launch_bounds__(Cfg<D, GROUPS>::NT, 1)
             const int ke = min(p.key_tiles, kb + count - n);
             const int nq = min(CN, a.B - qt * QT - c0);  // queries of this unit and group
             float l[CN];
+            bool folded = false;  // whether O^T's total holds anything
 #pragma unroll
             for (int i = 0; i < CN; ++i) l[i] = 0.f;
+            auto o_sum = [&](float (&o)[CN]) {  // the small parts first
+                tmem_ld16_wait(tbase + C::T_O + (PARTS - 1) * QT + c0 + lane_off, o);
+#pragma unroll 1
+                for (int part = PARTS - 2; part >= (folded ? -1 : 0); --part) {
+                    float x[CN];
+                    tmem_ld16_wait(tbase + (part < 0 ? C::T_T : C::T_O + part * QT) + c0 + lane_off, x);
+#pragma unroll
+                    for (int i = 0; i < CN; ++i) o[i] += x[i];
+                }
+            };
             for (int kt = kb; kt < ke; ++kt, ++n) {
                 const bool first = kt == kb, tail = (kt + 1) * KT > a.prefix_len;
                 const bool live = !tail || kt * KT + gt < a.prefix_len;
@@ -385,7 +402,7 @@ __global__ void __launch_bounds__(Cfg<D, GROUPS>::NT, 1)
 #pragma unroll
                     for (int i = 0; i < CN; i += 2) asm("max.f32 %0, %0, %1, %2;" : "+f"(top) : "f"(z[i]), "f"(z[i + 1]));
                 }
-                if (group_any(grp, first || top > SLACK)) {
+                if (group_any(grp, first || n % FOLD == 0 || top > SLACK)) {
                     logits();
                     const float mine = warp_reduce<false>(z);
                     if (lane < CN) sR[(warp % 4) * QN + c0 + lane] = mine;
@@ -404,18 +421,18 @@ __global__ void __launch_bounds__(Cfg<D, GROUPS>::NT, 1)
                         fence_after_sync();
 #pragma unroll
                         for (int i = 0; i < CN; ++i) l[i] *= sF[c0 + i];
-#pragma unroll 1
-                        for (int part = 0; part < PARTS; ++part) {
-                            const uint32_t at = tbase + C::T_O + part * QT + c0 + lane_off;
-                            float o[CN];
-                            tmem_ld16_wait(at, o);
+                        float o[CN];
+                        o_sum(o);
+                        folded = true;
 #pragma unroll
-                            for (int i = 0; i < CN; i += 8) {
-                                uint32_t r[8];
+                        for (int i = 0; i < CN; i += 8) {
+                            uint32_t r[8], zero[8] = {};
 #pragma unroll
-                                for (int e = 0; e < 8; ++e) r[e] = __float_as_uint(o[i + e] * sF[c0 + i + e]);
-                                tmem_st8(at + i, r);
-                            }
+                            for (int e = 0; e < 8; ++e) r[e] = __float_as_uint(o[i + e] * sF[c0 + i + e]);
+                            tmem_st8(tbase + C::T_T + c0 + i + lane_off, r);
+#pragma unroll
+                            for (int part = 0; part < PARTS; ++part)
+                                tmem_st8(tbase + C::T_O + part * QT + c0 + i + lane_off, zero);
                         }
                         tmem_wait_st();
                     }
@@ -469,14 +486,8 @@ __global__ void __launch_bounds__(Cfg<D, GROUPS>::NT, 1)
             const long long piece = (long long)blockIdx.x + u;
             {
                 const int dim = D == 128 ? gt : 16 * (warp % 4) + lane;
-                float v[CN], v2[CN];
-                tmem_ld16_wait(tbase + C::T_O + (PARTS - 1) * QT + c0 + lane_off, v);  // the small parts first
-#pragma unroll
-                for (int part = PARTS - 2; part >= 0; --part) {
-                    tmem_ld16_wait(tbase + C::T_O + part * QT + c0 + lane_off, v2);
-#pragma unroll
-                    for (int i = 0; i < CN; ++i) v[i] += v2[i];
-                }
+                float v[CN];
+                o_sum(v);
                 if (D == 128 || lane < 16) {
 #pragma unroll
                     for (int i = 0; i < CN; ++i)

@@ -71,3 +71,37 @@ def test_queries_and_weights_meet_the_prefix_in_fp32(P, B, gate, dtype, d):
     err = (out.double()[dim, :, dim] - ref).abs()
     worst = (err / tol).max().item()
     assert worst <= 1, f"off by {worst} of what fp32 weights and queries may be"
+
+
+@pytest.mark.parametrize("B,d", [(5, 64), (40, 64), (3, 128)])
+def test_long_sums_over_a_prefix_do_not_drift(P, B, d):
+    """Weighted values of one sign over a long prefix (832 steps of 16 keys a block), cancelled by two
+    rows of the sequence's own. The tensor cores cut each step's sum to fp32, up to 2^-23 of what
+    has been added up, all in one direction; parts of a sum are therefore joined by rounded
+    additions, and 64 steps lie between. What is added up since rises from nothing, so they cut
+    33 times 2^-23 of the whole at most; additions of up to 14 parts and of the pieces are
+    rounded (16 times 2^-24), the weights are off by 2^-20 (as above)."""
+    H, n, page = 30, 65536, 1024
+    c = Cache([1] * B, H, d, page, BF, True, seed=d, prefix=n)
+    pre = c.prefix_table.long()
+    c.v[pre] = (1 + torch.rand(c.v[pre].shape, device="cuda", generator=c.rng)).to(BF)
+    c.gs.zero_()
+    x = c.step_inputs()
+    x["q"].zero_()
+    x["log_f"].zero_()
+    own = torch.tensor([c.pages(r)[0] for r in c.slot], device="cuda")
+    c.g[own, :, 0] = 0.0
+    w = c.rows(c.g, None, n).exp()  # of the prefix; an own row weighs 1
+    total = w.sum(-1, keepdim=True) + 2
+    s = torch.stack([w[h] @ c.v[pre, h].reshape(-1, d)[:n].double() for h in range(H)])
+    bf = lambda t: t.to(BF).double()
+    v1 = -bf(s)
+    v0 = -bf(s + v1)
+    x["v_new"][:] = v1.to(BF)
+    c.v[own, :, 0] = v0.to(BF)
+    out = c.call(P, x, scale=1.0)
+    ref = (s + v1 + v0) / total
+    eps = 33 * 2.0 ** -23 + 16 * 2.0 ** -24 + 2.0 ** -20
+    tol = 2 * s / total * eps + 2.0 ** -8 * ref.abs()
+    worst = ((out.double() - ref).abs() / tol).max().item()
+    assert worst <= 1, f"off by {worst} of the bound"

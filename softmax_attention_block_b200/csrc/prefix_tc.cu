@@ -196,10 +196,9 @@ __global__ void __launch_bounds__(Cfg<D, GROUPS>::NT, 1)
             }
             const int key0 = kt * KT;
             if (n == 0 || kt == 0) {
-                if (seg > 0 && !mbar_wait(q_empty, (seg - 1) & 1, WAIT_LIMIT_NS)) {
-                    ok = false;
-                    break;
-                }
+                // lanes may run out of time one by one: they go on, or leave, together
+                ok = __all_sync(0xffffffffu, seg == 0 || mbar_wait(q_empty, (seg - 1) & 1, WAIT_LIMIT_NS));
+                if (!ok) break;
                 if (seg == 0) wait_previous();  // the queries; keys and values are nobody's output
                 if (lane == 0) {
                     mbar_expect_tx(q_full, C::Q);

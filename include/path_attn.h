@@ -492,6 +492,9 @@ int path_profile_read(path_stage_time *out, int max_entries);
  * context stays usable. The producer still waits for every copy it did issue
  * before its block exits. Needs L > 128 (at least two query tiles). Returns
  * PATH_OK, or PATH_ERR_INVALID_ARG if `on` is not 0 or 1.
+ * The paged decode steps listen to it as well: the load of the own part's second granule (8 or
+ * 16 rows, in the first warp) never completes, waits are as short, and the rows and heads that
+ * this warp works on from there are NaN.
  */
 path_status path_test_withhold_kv_load(int on);
 

@@ -31,7 +31,8 @@ Entry points (same names as the C ABI):
   (a batch behind one shared prefix), ``path_pages_reserve``, ``path_pages_fork``,
   ``path_pages_free``, ``path_pages_compact``, ``path_pages_copy``, ``path_pages_store``,
   ``path_state_copy``, ``path_decode_paged_workspace_bytes``
-- test hook: ``path_test_withhold_kv_load(on)`` (makes the forward's bounded waits give up)
+- test hook: ``path_test_withhold_kv_load(on)`` (makes bounded waits of the forward and the
+  paged decode steps give up)
 """
 from __future__ import annotations
 
@@ -447,7 +448,8 @@ def path_attn_prefill(q, k, v, w, beta, capacity, log_f=None, scale=None, out=No
 
 def path_test_withhold_kv_load(on: bool) -> None:
     """Test hook of the bounded waits (include/path_attn.h): while on, the tensor-core
-    forward's last query tile never receives one key/value block and reports a timeout."""
+    forward's last query tile never receives one key/value block and reports a timeout; so does
+    the paged decode steps' first warp."""
     st = lib().path_test_withhold_kv_load(1 if on else 0)
     if st:
         raise PathError(st, "path_test_withhold_kv_load")

@@ -3,6 +3,7 @@
 
 #include "paged.cuh"
 #include "runtime.cuh"
+#include "tc.cuh"
 
 using namespace path;
 
@@ -75,6 +76,8 @@ path_status step_args(const void *q, const void *k_new, const void *v_new, const
     a.H = H;
     a.c = PagedCache{rows, n_slots, table, max_pages, lens, page_log2(page), n_pages, k_pages, v_pages, g_pages};
     a.out = out;
+    a.withhold = withhold_kv_load();
+    a.limit_ns = a.withhold ? 2000000ull : tc::WAIT_LIMIT_NS;
     return PATH_OK;
 }
 

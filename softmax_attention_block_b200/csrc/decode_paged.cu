@@ -242,6 +242,7 @@ __global__ void __launch_bounds__(OwnCfg<T, D>::NT, 1) decode_own_kernel(PagedSt
         __syncthreads();
     }
     tc::fence_async_smem();  // s_cum's place now belongs to the copies
+    if (a.withhold && blockIdx.x == 0 && tid == 0) tc::mbar_expect_more(&s_bar[0][1], 16);  // bytes that never come
 
     if (cc.left > 0) {
         const float scale2 = a.scale * LOG2E;
@@ -319,7 +320,17 @@ __global__ void __launch_bounds__(OwnCfg<T, D>::NT, 1) decode_own_kernel(PagedSt
         float beta = 0.f, lf = 0.f, m = -INFINITY, l = 0.f;
         F2 q[8], w[8], acc[8];
         while (cc.left > 0) {
-            if (!tc::mbar_wait(&s_bar[warp][st], parity, dead ? 0 : tc::WAIT_LIMIT_NS)) dead = true;
+            if (!tc::mbar_wait(&s_bar[warp][st], parity, dead ? 0 : a.limit_ns)) {
+                // Nothing more is worked on or loaded, but copies may still be on their way into this
+                // block's memory: for this granule and the ring behind it (less of it at a share's end,
+                // where the waits for the rest run out of time).
+                if (!dead) {
+#pragma unroll 1
+                    for (int i = 0; i < S; ++i)
+                        tc::mbar_wait(&s_bar[warp][(st + i) % S], st + i < S ? parity : parity ^ 1, a.limit_ns);
+                }
+                dead = true;
+            }
             dead = __any_sync(0xffffffffu, dead);
             const long long row0 = s_row[warp][st];
             const int r0 = cc.j * GR, n = cc.n;
@@ -508,9 +519,6 @@ __global__ void __launch_bounds__(OwnCfg<T, D>::NT, 1) decode_own_kernel(PagedSt
                 }
             }
         }
-        if (dead)  // copies may still be on their way into this block's memory
-            for (int i = 0; i < S; ++i)
-                tc::mbar_wait(&s_bar[warp][(st + i) % S], st + i < S ? parity : parity ^ 1, tc::WAIT_LIMIT_NS);
     }
     // this kernel needs nothing of the ones before it in the call, but completes after them
     if (SHARED && tid == 0) wait_previous();

@@ -33,6 +33,8 @@ struct PagedStep {
     int prefix_len;
     float *state;    // [n_slots, H, d, d] products of the Householder factors
     float *g_state;  // [n_slots, H]
+    unsigned long long limit_ns;  // of a wait on a barrier
+    int withhold;  // test hook: one load of the first block never completes
 };
 
 // slot of batch row b: negative if idle, or invalid (see row_ok)

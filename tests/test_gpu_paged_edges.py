@@ -105,3 +105,64 @@ def test_long_sums_over_a_prefix_do_not_drift(P, B, d):
     tol = 2 * s / total * eps + 2.0 ** -8 * ref.abs()
     worst = ((out.double() - ref).abs() / tol).max().item()
     assert worst <= 1, f"off by {worst} of the bound"
+
+
+TIMEOUT = 5
+
+
+def same(a, b):
+    return torch.equal(torch.nan_to_num(a.float(), nan=1e9), torch.nan_to_num(b.float(), nan=1e9))
+
+
+def restore(c, snap):
+    for name, t in zip(("k", "v", "g", "state", "gs"), snap):
+        if t is not None:
+            getattr(c, name).copy_(t)
+
+
+def withheld_step(P, c, x, prefix=0):
+    """The step three times from one state: undisturbed, with a load withheld, undisturbed again.
+    The last is the first bit for bit; returns the two outputs and the pools after the second."""
+    ws = torch.empty(P.path_decode_paged_workspace_bytes(len(c.slot), c.H, c.M, c.page, c.d, c.dtype, prefix),
+                     dtype=torch.uint8, device="cuda")
+    start = c.snap()
+    want = c.call(P, x, workspace=ws)
+    after = c.snap()
+    assert P.path_attn_wait_status(ws) == 0
+    restore(c, start)
+    P.path_test_withhold_kv_load(True)
+    try:
+        out = c.call(P, x, workspace=ws)
+        torch.cuda.synchronize()
+        status = P.path_attn_wait_status(ws)
+    finally:
+        P.path_test_withhold_kv_load(False)
+    assert status == TIMEOUT
+    given_up = c.snap()
+    restore(c, start)
+    again = c.call(P, x, workspace=ws)
+    assert P.path_attn_wait_status(ws) == 0
+    assert same(again, want)
+    for a, b in zip(after, c.snap()):
+        assert a is None or same(a, b)
+    return want, out, after, given_up
+
+
+@pytest.mark.parametrize("d,dtype,gate,prefix,n", [
+    (64, BF, True, 0, 2000),   # shares of about 22 granules, rings of 4
+    (128, BF, False, 0, 1300),
+    (64, F32, True, 0, 1300),
+    (128, F32, False, 65, 300),
+])
+def test_an_own_part_that_gives_up(P, d, dtype, gate, prefix, n):
+    """The first warp never gets its second granule: its unit is NaN, the others and the calls after it
+    are as ever, and the report says so."""
+    c = Cache([n] * 40, 8, d, 64, dtype, gate, seed=1, prefix=prefix)
+    want, out, after, given_up = withheld_step(P, c, c.step_inputs(), prefix)
+    assert torch.isnan(out[0, 0]).all()
+    assert same(out[0, 1:], want[0, 1:]) and same(out[1:], want[1:])
+    p0 = c.pages(c.slot[0])[0]
+    a, b = after[0], given_up[0]
+    assert same(a[p0, 0, :8], b[p0, 0, :8]), "the granule before it"
+    assert not same(a[p0, 0, 16:], b[p0, 0, 16:]), "keys that were never there"
+    assert same(a[:, 1:], b[:, 1:]) and all(x is None or same(x, y) for x, y in zip(after[3:], given_up[3:]))

@@ -494,7 +494,9 @@ int path_profile_read(path_stage_time *out, int max_entries);
  * PATH_OK, or PATH_ERR_INVALID_ARG if `on` is not 0 or 1.
  * The paged decode steps listen to it as well: the load of the own part's second granule (8 or
  * 16 rows, in the first warp) never completes, waits are as short, and the rows and heads that
- * this warp works on from there are NaN.
+ * this warp works on from there are NaN. Behind a PATH_BF16 prefix neither does the load of the
+ * first block's second tile of 128 keys: the rows that share a tile of queries with row 0 are
+ * NaN at head 0.
  */
 path_status path_test_withhold_kv_load(int on);
 

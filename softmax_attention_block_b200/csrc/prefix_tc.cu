@@ -165,6 +165,7 @@ __global__ void __launch_bounds__(Cfg<D, GROUPS>::NT, 1)
         }
         mbar_init(mma_done, 2);
         mbar_fence_init();
+        if (a.withhold && blockIdx.x == 0) mbar_expect_more(&k_full[1], 16);  // bytes that never come
         *s_bad = 0;
     }
     if (warp == W_O) tmem_alloc(tmem_slot, C::TMEM);
@@ -197,7 +198,7 @@ __global__ void __launch_bounds__(Cfg<D, GROUPS>::NT, 1)
             const int key0 = kt * KT;
             if (n == 0 || kt == 0) {
                 // lanes may run out of time one by one: they go on, or leave, together
-                ok = __all_sync(0xffffffffu, seg == 0 || mbar_wait(q_empty, (seg - 1) & 1, WAIT_LIMIT_NS));
+                ok = __all_sync(0xffffffffu, seg == 0 || mbar_wait(q_empty, (seg - 1) & 1, a.limit_ns));
                 if (!ok) break;
                 if (seg == 0) wait_previous();  // the queries; keys and values are nobody's output
                 if (lane == 0) {
@@ -222,7 +223,7 @@ __global__ void __launch_bounds__(Cfg<D, GROUPS>::NT, 1)
             const int cnt = __popc(__ballot_sync(0xffffffffu, good));
             const int row = good ? (int)((((long long)pid * a.H + h) << log2p) + (key & (page - 1))) : 0;
             const uint32_t ks = (uint32_t)n % NK, vs = (uint32_t)n % NV, gs = (uint32_t)n % NG;
-            if (n >= NK && !mbar_wait(&k_empty[ks], (n / NK - 1) & 1, WAIT_LIMIT_NS)) ok = false;
+            if (n >= NK && !mbar_wait(&k_empty[ks], (n / NK - 1) & 1, a.limit_ns)) ok = false;
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             if (lane == 0) {
@@ -237,7 +238,7 @@ __global__ void __launch_bounds__(Cfg<D, GROUPS>::NT, 1)
                 if (gate) bulk_load(sG + gs * KT + lane * box, a.c.g + row, box * 4, &k_full[ks]);
             }
             issued_k = n + 1;
-            if (n >= NV && !mbar_wait(&v_empty[vs], (n / NV - 1) & 1, WAIT_LIMIT_NS)) ok = false;
+            if (n >= NV && !mbar_wait(&v_empty[vs], (n / NV - 1) & 1, a.limit_ns)) ok = false;
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             if (lane == 0) {
@@ -251,13 +252,12 @@ __global__ void __launch_bounds__(Cfg<D, GROUPS>::NT, 1)
             }
             issued_v = n + 1;
         }
-        if (!ok) {  // leave no copy on its way into this block's memory
-            for (int n = max(0, issued_k - NK); n < issued_k; ++n)
-                mbar_wait(&k_full[n % NK], (n / NK) & 1, WAIT_LIMIT_NS);
-            for (int n = max(0, issued_v - NV); n < issued_v; ++n)
-                mbar_wait(&v_full[n % NV], (n / NV) & 1, WAIT_LIMIT_NS);
-            if (seg > 0) mbar_wait(q_full, (seg - 1) & 1, WAIT_LIMIT_NS);
-        }
+        // leave no copy on its way into this block's memory: whoever waited for it may have given up
+        for (int n = max(0, issued_k - NK); n < issued_k; ++n)
+            mbar_wait(&k_full[n % NK], (n / NK) & 1, 8 * a.limit_ns);
+        for (int n = max(0, issued_v - NV); n < issued_v; ++n)
+            mbar_wait(&v_full[n % NV], (n / NV) & 1, 8 * a.limit_ns);
+        if (seg > 0) mbar_wait(q_full, (seg - 1) & 1, 8 * a.limit_ns);
     } else if (warp == W_S) {
         // S^T = K . qt^T, lo, mid, hi: the sum that a step cuts is small until hi comes. The whole warp runs along, converged, and one lane issues:
         // descriptors stay uniform, and differ from a base by the address in their low bits.
@@ -268,10 +268,10 @@ __global__ void __launch_bounds__(Cfg<D, GROUPS>::NT, 1)
         bool ok = true;
         for (int n = 0; n < count; ++n) {
             const uint32_t ks = (uint32_t)n % NK;
-            if (n == 0 || kt == 0) ok = mbar_wait(q_full, seg++ & 1, WAIT_LIMIT_NS);
-            ok = ok && mbar_wait(&k_full[ks], (n / NK) & 1, WAIT_LIMIT_NS);
+            if (n == 0 || kt == 0) ok = mbar_wait(q_full, seg++ & 1, a.limit_ns);
+            ok = ok && mbar_wait(&k_full[ks], (n / NK) & 1, a.limit_ns);
             // the buffer of S^T was read before the weights of tile n - 2 were complete
-            if (n >= 2) ok = ok && mbar_wait(&p_full[n & 1], ((n >> 1) - 1) & 1, WAIT_LIMIT_NS);
+            if (n >= 2) ok = ok && mbar_wait(&p_full[n & 1], ((n >> 1) - 1) & 1, a.limit_ns);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             fence_after_sync();
@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(Cfg<D, GROUPS>::NT, 1)
         }
         // the tensor memory is freed after the issuing warps leave: no MMA may still be running then
         commit_if(issue, mma_done);
-        mbar_wait(mma_done, 0, 8 * WAIT_LIMIT_NS);
+        mbar_wait(mma_done, 0, 8 * a.limit_ns);
     } else if (warp == W_O) {
         // O^T += V^T . P, hi | mid | lo as columns
         const uint32_t issue = lane == 0;
@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(Cfg<D, GROUPS>::NT, 1)
         bool ok = true;
         for (int n = 0; n < count; ++n) {
             const uint32_t vs = (uint32_t)n % NV;
-            ok = mbar_wait(&v_full[vs], (n / NV) & 1, WAIT_LIMIT_NS) && mbar_wait(&p_full[n & 1], (n >> 1) & 1, WAIT_LIMIT_NS);
+            ok = mbar_wait(&v_full[vs], (n / NV) & 1, a.limit_ns) && mbar_wait(&p_full[n & 1], (n >> 1) & 1, a.limit_ns);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             fence_after_sync();
@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(Cfg<D, GROUPS>::NT, 1)
             commit_if(issue, &o_done[n & 1]);
         }
         commit_if(issue, mma_done);
-        mbar_wait(mma_done, 0, 8 * WAIT_LIMIT_NS);
+        mbar_wait(mma_done, 0, 8 * a.limit_ns);
     } else {
         // thread = key of the tile (a lane of S^T), queries c0 .. c0 + 15; then a row of O^T: dim gt,
         // or at D = 64 dim 16 (warp % 4) + lane in the lanes below 16. Waits that give up leave a mark
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(Cfg<D, GROUPS>::NT, 1)
         const float scale2 = a.scale * LOG2E;
         bool gave_up = false;
         auto wait = [&](uint64_t *bar, uint32_t parity) {
-            if (!mbar_try_wait(bar, parity) && !gave_up) gave_up = !mbar_wait(bar, parity, WAIT_LIMIT_NS);
+            if (!mbar_try_wait(bar, parity) && !gave_up) gave_up = !mbar_wait(bar, parity, a.limit_ns);
             __syncwarp();
         };
         auto product_done = [&](int i) { wait(&o_done[i & 1], (i >> 1) & 1); };

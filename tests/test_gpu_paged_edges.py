@@ -166,3 +166,16 @@ def test_an_own_part_that_gives_up(P, d, dtype, gate, prefix, n):
     assert same(a[p0, 0, :8], b[p0, 0, :8]), "the granule before it"
     assert not same(a[p0, 0, 16:], b[p0, 0, 16:]), "keys that were never there"
     assert same(a[:, 1:], b[:, 1:]) and all(x is None or same(x, y) for x, y in zip(after[3:], given_up[3:]))
+
+
+@pytest.mark.parametrize("B,d,gate", [(5, 64, True), (40, 64, False), (64, 64, True), (20, 128, True), (40, 128, False),
+                                      (9, 128, True)])
+def test_a_prefix_that_gives_up(P, B, d, gate):
+    """The first block never gets its second tile of keys: head 0 is NaN, all else is as ever, in this call
+    and the next. (The own parts are one granule each, which the hook passes over.)"""
+    c = Cache([0] * B, 8, d, 64, BF, gate, seed=B, prefix=40000)
+    want, out, after, given_up = withheld_step(P, c, c.step_inputs(), 40000)
+    assert torch.isnan(out[:, 0]).all()
+    assert same(out[:, 1:], want[:, 1:])
+    for a, b in zip(after, given_up):
+        assert a is None or same(a, b)

@@ -259,7 +259,10 @@ path_status path_decode_step_gated(const void *q, const void *k_new, const void 
  * k_cache, v_cache: [B,H,capacity,d] in the input element type (fp32 for
  * PATH_F32, bf16 for PATH_BF16 and PATH_BF16_F32OUT), 16-byte aligned;
  * g_cache: [B,H,capacity] fp32, NULL iff log_f is NULL. Only rows 0..L-1 are
- * written. Requires d in {64, 128} (the decode head dims; else
+ * written. Every row of the batch is carried to position L-1: where sequences of
+ * different lengths are padded to one L, beta = 0 and log_f = 0 behind a row's
+ * end (and finite q, k, v, w) leave its keys and biases as they are there; with
+ * anything else the padding's factors are in them. Requires d in {64, 128} (the decode head dims; else
  * PATH_ERR_UNSUPPORTED) and L <= capacity (else PATH_ERR_INVALID_ARG). The
  * caches must not alias the inputs.
  */
@@ -399,6 +402,8 @@ path_status path_pages_copy(const int *moves, int max_moves, int *info, void *k_
  * Writes the first tokens[b] rows of a contiguous cache (k_cache, v_cache
  * [B,H,capacity,d], g_cache [B,H,capacity]: what path_attn_prefill leaves) into the pages
  * of slot rows[b] (b if rows is NULL), from its row 0; g_cache and g_pages go together.
+ * They are copied as they are: a prefill of padded rows needs beta = 0 and log_f = 0 behind
+ * tokens[b] (see path_attn_prefill).
  * Rows behind tokens[b] keep what they held. A slot, count (0 to capacity and
  * max_pages * page) or page out of range is skipped and sets info[0] to PATH_ERR_PAGE if
  * info is not NULL (it is not cleared otherwise). lens is the caller's.

@@ -412,7 +412,8 @@ def path_attn_prefill(q, k, v, w, beta, capacity, log_f=None, scale=None, out=No
     caches [B,H,capacity,d] in q's dtype with rows 0..L-1 written (k_cache row j =
     H_{L-1} ... H_{j+1} k_j, v_cache row j = v_j); g_cache [B,H,capacity] fp32 (row j =
     c_{L-1} - c_j) with the forget gate, else None. Caches the call allocates are
-    zero past row L-1."""
+    zero past row L-1. Rows padded to one L need beta = 0 and log_f = 0 behind their ends, so
+    that the padding's factors stay out of their keys."""
     _check_attn_inputs(q, k, v, w, beta, log_f)
     B, H, L, d = q.shape
     if out is None:
@@ -658,7 +659,8 @@ def path_pages_copy(moves, info, k_pages, v_pages, g_pages=None):
 def path_pages_store(k_cache, v_cache, k_pages, v_pages, table, rows, tokens, g_cache=None,
                      g_pages=None, info=None):
     """Writes rows 0..tokens[b]-1 of the contiguous caches [B,H,capacity,d] (path_attn_prefill's)
-    into the pages of slot rows[b] (None: b). info [4] int32, if given, reports PATH_ERR_PAGE in
+    into the pages of slot rows[b] (None: b), as they are: a prefill of padded rows needs beta = 0
+    and log_f = 0 behind tokens[b]. info [4] int32, if given, reports PATH_ERR_PAGE in
     info[0]."""
     if k_cache.dim() != 4:
         raise ValueError("k_cache must be [B,H,capacity,d]")

@@ -6,6 +6,7 @@ import math
 import pytest
 import torch
 
+import oracle
 from test_gpu_paged import BF, F32, Cache, P, ints  # noqa: F401 (P: the fixture)
 
 pytestmark = pytest.mark.gpu
@@ -179,3 +180,53 @@ def test_a_prefix_that_gives_up(P, B, d, gate):
     assert same(out[:, 1:], want[:, 1:])
     for a, b in zip(after, given_up):
         assert a is None or same(a, b)
+
+
+@pytest.mark.parametrize("d,dtype,gate", [(64, BF, True), (64, F32, False), (128, BF, False), (128, F32, True)])
+def test_a_padded_prefill_in_pages(P, d, dtype, gate):
+    """Prompts of different lengths in one prefill, padded with beta = 0 and log f = 0, stored into
+    pages and continued. Every output is the oracle's row of that sequence alone. The bars are the
+    decode tests': 1e-4 at fp32, 2e-2 at bf16."""
+    H, page, lens, steps = 2, 32, [150, 1, 77, 128], 3
+    B, L = len(lens), max(lens)
+    g = torch.Generator().manual_seed(d)
+    n = L + steps
+    x = {a: torch.randn((B, H, n, d), generator=g) for a in "qkvw"}
+    x["w"] /= x["w"].norm(dim=-1, keepdim=True)
+    x = {a: t.to(dtype) for a, t in x.items()}
+    x["beta"] = 1.9 * torch.sigmoid(torch.randn((B, H, n), generator=g))
+    x["log_f"] = torch.nn.functional.logsigmoid(torch.randn((B, H, n), generator=g) + 2)
+    # the prompts are the sequences' first rows; what stands behind them in the prefill is padding
+    pad = {a: t[:, :, :L].clone() for a, t in x.items()}
+    for b, m in enumerate(lens):
+        pad["beta"][b, :, m:] = 0
+        pad["log_f"][b, :, m:] = 0
+        for a in "qkvw":
+            pad[a][b, :, m:] = torch.randn((H, L - m, d), generator=g).to(dtype)
+    pad = {a: t.contiguous().cuda() for a, t in pad.items()}
+    out, _, kc, vc, gc = P.path_attn_prefill(*(pad[a] for a in ("q", "k", "v", "w", "beta")), L + 4,
+                                             log_f=pad["log_f"] if gate else None)
+    M = n // page + 1
+    N = B * M
+    table = torch.randperm(N, generator=g).view(B, M).int().cuda()
+    kp, vp = (torch.full((N, H, page, d), math.nan, dtype=dtype, device="cuda") for _ in range(2))
+    gp = torch.full((N, H, page), math.nan, device="cuda") if gate else None
+    info, slot_len = ints([0] * 4), ints(lens)
+    P.path_pages_store(kc, vc, kp, vp, table, None, slot_len, g_cache=gc, g_pages=gp, info=info)
+    assert info.tolist()[0] == 0
+    bar = 1e-4 if dtype == F32 else 2e-2
+    refs = []
+    for b, m in enumerate(lens):
+        seq = {a: t[b:b + 1, :, :m + steps] for a, t in x.items()}
+        ref, _ = oracle.fwd(seq["q"], seq["k"], seq["v"], seq["w"], seq["beta"], seq["log_f"] if gate else None)
+        refs.append(torch.as_tensor(ref[0]))
+        err = (out[b, :, :m].double().cpu() - refs[b][:, :m]).abs().max().item()
+        assert err <= bar, f"prefill, row {b}: {err}"
+    for t in range(steps):
+        col = lambda a: torch.stack([x[a][b, :, m + t] for b, m in enumerate(lens)]).cuda()
+        o = P.path_decode_step_paged(col("q"), col("k"), col("v"), col("w"), col("beta"), kp, vp, table, slot_len,
+                                     log_f=col("log_f") if gate else None, g_pages=gp)
+        slot_len += 1
+        for b, m in enumerate(lens):
+            err = (o[b].double().cpu() - refs[b][:, m + t]).abs().max().item()
+            assert err <= bar, f"step {t}, row {b}: {err}"

@@ -224,3 +224,24 @@ def test_table_checks():
         P.path_state_copy(z(R, H, D, D + 1, dt=torch.float32), a, a)
     with pytest.raises(ValueError, match="CUDA tensors"):
         P.path_state_copy(z(R, H, D, D, dt=torch.float32), a, a)
+
+
+def test_the_readme_step_advances_the_rows_it_names():
+    """README's step as it stands there, its calls replaced: with idle rows in the batch it asks for one
+    token more for each slot in it and advances these slots' lengths, no other's."""
+    import os
+    import types
+
+    text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")).read()
+    block = text.split("## A server's step")[1].split("\n\n    ")[1].split("\n\n")[0]
+    asked = []
+    names = dict(torch=torch, q=0, k=0, v=0, w=0, beta=0, k_pages=0, v_pages=0, ws=0, page=16, state=0, held=0,
+                 owner=0, prefix_len=20, prefix_slot=3, table=z(5, 2, dt=I32))
+    names["lens"] = torch.tensor([7, 8, 9, 10, 11], dtype=I32)
+    names["rows"] = torch.tensor([2, -1, 0, -7], dtype=I32)
+    names["path_pages_reserve"] = lambda t, h, o, p, rows, tokens: asked.append((rows, tokens))
+    names["path_decode_step_shared"] = lambda *a, **kw: types.SimpleNamespace()
+    exec("import torch\n" + "\n".join(line.removeprefix("    ") for line in block.split("\n")), names)
+    rows, tokens = asked[0]
+    assert tokens.dtype == I32 and [int(n) for r, n in zip(rows, tokens) if r >= 0] == [10, 8]
+    assert names["lens"].tolist() == [8, 8, 10, 10, 11]

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import oracle
-from test_gpu_paged import BF, F32, Cache, P, ints  # noqa: F401 (P: the fixture)
+from test_gpu_paged import BF, F32, Cache, P, ints, run_steps  # noqa: F401 (P: the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -230,3 +230,169 @@ def test_a_padded_prefill_in_pages(P, d, dtype, gate):
         for b, m in enumerate(lens):
             err = (o[b].double().cpu() - refs[b][:, m + t]).abs().max().item()
             assert err <= bar, f"step {t}, row {b}: {err}"
+
+
+# ------------------------------------------------------------------ layouts that only large batches take
+@pytest.mark.parametrize("prefix", [0, 300])
+@pytest.mark.parametrize("gate", [False, True])
+@pytest.mark.parametrize("rows,few", [(12, False), (13, True), (24, True)])
+def test_both_layouts_of_rows_of_128_bytes(P, rows, few, gate, prefix):
+    """bf16, head dim 64: from 40 granules for each of eight warps an SM, eight warps work with longer
+    rings, below it twelve (a granule is 16 rows, and a unit counts one more)."""
+    H, lens = 24, [1500 + 997 * i % 1000 for i in range(rows)]
+    total = H * sum(n // 16 + 2 for n in lens)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert (total >= sms * 8 * 40) == few
+    run_steps(P, Cache(lens, H, 64, 64, BF, gate, seed=rows, prefix=prefix), steps=1)
+
+
+@pytest.mark.parametrize("prefix,lens,dtype,d", [
+    (20000, [5, 0, 70], F32, 64),              # 296 blocks hold a piece of each row
+    (20000, [5, 0, 70], F32, 128),
+    (0, [100000] + [0] * 299, BF, 64),         # many units, so 64 or 128 threads join; over 128 pieces of one
+    (0, [100000] + [0] * 299, BF, 128),
+    (0, [60000] + [0] * 299, F32, 128),
+])
+def test_units_of_more_pieces_than_threads(P, prefix, lens, dtype, d):
+    run_steps(P, Cache(lens, 1, d, 64, dtype, False, seed=d, prefix=prefix), steps=1)
+
+
+@pytest.mark.parametrize("dtype,N", [(BF, 9000), (F32, 8400)])
+def test_a_prefix_beyond_32_bit_offsets(P, dtype, N):
+    """Pages of a sequence and of its prefix at the end of a pool of more than 2^31 elements."""
+    H, page, d = 32, 64, 128
+    assert N * H * page * d > 2 ** 31
+    k = torch.empty((N, H, page, d), dtype=dtype, device="cuda")
+    v = torch.empty_like(k)
+    g = torch.empty((N, H, page), device="cuda")
+    c = Cache([100, 3], H, d, page, dtype, True, seed=8, prefix=1000)
+    used = sorted({p for r in c.slot for p in c.pages(r) if p >= 0} | set(c.pages(None)))
+    table, pre = c.table.clone(), c.prefix_table.clone()
+    for i, p in enumerate(used):
+        k[N - 1 - i], v[N - 1 - i], g[N - 1 - i] = c.k[p], c.v[p], c.g[p]
+        table[c.table == p] = N - 1 - i
+        pre[c.prefix_table == p] = N - 1 - i
+    x, state, gs = c.step_inputs(), c.state.clone(), c.gs.clone()
+    out = P.path_decode_step_shared(x["q"], x["k_new"], x["v_new"], x["w"], x["beta"], k, v, table, c.lens, pre,
+                                    1000, state, rows=ints(c.slot), log_f=x["log_f"], g_pages=g, g_state=gs)
+    want = c.call(P, x)
+    assert torch.equal(out, want) and torch.equal(state, c.state) and torch.equal(gs, c.gs)
+    for i, p in enumerate(used):
+        assert same(k[N - 1 - i], c.k[p]) and same(v[N - 1 - i], c.v[p]) and same(g[N - 1 - i], c.g[p])
+
+
+# ------------------------------------------------------------------ bad pages, infinities, equal logits
+@pytest.mark.parametrize("gate", [False, True])
+@pytest.mark.parametrize("d,dtype", [(64, BF), (128, BF), (64, F32), (128, F32)])
+@pytest.mark.parametrize("prefix", [0, 500])
+def test_bad_pages_in_every_form(P, prefix, d, dtype, gate):
+    """A page out of range in the table or in the prefix's, first, in the middle or last: NaN where it
+    belongs, the report, and all else bit for bit as without it."""
+    lens, H, page = [40, 170, 33], 3, 32
+    fresh = lambda: Cache(lens, H, d, page, dtype, gate, prefix=prefix, seed=5)
+    c = fresh()
+    x, N = c.step_inputs(), c.k.shape[0]
+    want, good = c.call(P, x), c.snap()
+    places = [("table", (c.slot[1], j), [1], p) for j, p in ((0, -1), (2, N), (5, 2 ** 31 - 1))]
+    if prefix:
+        places += [("prefix_table", (j,), [0, 1, 2], p) for j, p in ((0, N), (7, -(2 ** 31)), (15, 2 ** 31 - 1))]
+    ws = torch.empty(P.path_decode_paged_workspace_bytes(3, H, c.M, page, d, dtype, prefix), dtype=torch.uint8,
+                     device="cuda")
+    for name, at, bad, p in places:
+        c = fresh()
+        getattr(c, name)[at] = p
+        out = c.call(P, x, workspace=ws)
+        assert P.path_attn_wait_status(ws) == 6
+        keep = torch.ones(N, dtype=torch.bool, device="cuda")
+        if name == "table":
+            keep[[q for q in fresh().pages(c.slot[1]) if q >= 0]] = False
+        for b in range(3):
+            if b in bad:
+                assert torch.isnan(out[b]).all()
+            else:
+                assert torch.equal(out[b], want[b])
+        for a, b in zip(c.snap()[:3], good[:3]):
+            assert a is None or same(a[keep], b[keep]), (name, at)
+
+
+@pytest.mark.parametrize("prefix", [0, 200])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_equal_logits(P, prefix, dtype):
+    """q = 0: the mean of all values."""
+    c = Cache([40, 70, 0], 3, 64, 32, dtype, False, prefix=prefix, seed=3)
+    before, x = c.snap(), c.step_inputs()
+    x["q"].zero_()
+    c.check(before, x, c.call(P, x))
+
+
+@pytest.mark.parametrize("prefix", [0, 200])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_infinities_stay_in_their_head(P, prefix, dtype):
+    """An infinite query, key or value in head 0 of a row, or of the prefix, changes no other head and no
+    other row; an infinite new value comes out as it is."""
+    inf = math.inf
+    fresh = lambda: Cache([40, 70], 3, 64, 32, dtype, True, prefix=prefix, seed=4)
+    c = fresh()
+    x0 = c.step_inputs()
+    want = c.call(P, x0)
+
+    def go(change):
+        c = fresh()
+        x = {a: t.clone() for a, t in x0.items()}
+        change(c, x)
+        return c.call(P, x)
+
+    row0 = c.pages(c.slot[0])[0]
+    pool = [("k", row0), ("v", row0)]
+    for name, p in pool:
+        def change(c, x):
+            getattr(c, name)[p, 0, 5, 7] = -inf
+        out = go(change)
+        assert torch.equal(out[1], want[1]) and torch.equal(out[0, 1:], want[0, 1:])
+        assert not torch.isfinite(out[0, 0]).all()
+    for name in ("q", "v_new"):
+        def change(c, x):
+            x[name][0, 0, 7] = inf
+        out = go(change)
+        assert torch.equal(out[1], want[1]) and torch.equal(out[0, 1:], want[0, 1:])
+        if name == "q":
+            assert torch.isnan(out[0, 0]).all()
+        else:
+            assert out[0, 0, 7] == inf and torch.equal(out[0, 0, 8:], want[0, 0, 8:])
+    if prefix:
+        for name in ("k", "v"):
+            def change(c, x):
+                getattr(c, name)[c.pages(None)[3], 0, 9, 7] = inf
+            out = go(change)
+            assert torch.equal(out[:, 1:], want[:, 1:])
+            if name == "v":
+                assert not torch.isfinite(out[:, 0, 7]).any() and torch.equal(out[:, 0, 8:], want[:, 0, 8:])
+
+
+def test_an_infinite_key_of_an_fp32_prefix(P):
+    """A logit of -inf leaves the other keys' weights as they are; one of +inf is NaN. With w = 0 and
+    the identity as state the queries meet the prefix as they are. Tolerances as for a step."""
+    n, d, B = 200, 64, 6
+    c = Cache([0] * B, 2, d, 32, F32, False, prefix=n, seed=7)
+    c.state.copy_(torch.eye(d, device="cuda").expand_as(c.state))
+    x = c.step_inputs()
+    x["w"].zero_()
+    c.k[c.pages(None)[3], 0, 9] = 0
+    c.k[c.pages(None)[3], 0, 9, 7] = math.inf
+    x["q"][:, 0, 7] = torch.tensor([1.0, -1, 0.5, -2, -0.25, 3], device="cuda")
+    out = c.call(P, x)
+    scale = d ** -0.5
+    for b in range(B):
+        q = x["q"][b, 0].double()
+        keys, vals = c.rows(c.k, None, n)[0], c.rows(c.v, None, n)[0]
+        there = torch.ones(n, dtype=torch.bool, device="cuda")
+        there[3 * 32 + 9] = False
+        if q[7] > 0:
+            assert torch.isnan(out[b, 0]).all()
+            continue
+        k = torch.cat([keys[there], x["k_new"][b, :1].double()])
+        v = torch.cat([vals[there], x["v_new"][b, :1].double()])
+        ref = torch.softmax(scale * (k @ q), 0) @ v
+        ez = scale * q.norm() * k.norm(dim=-1).max() * 8 * math.sqrt(d) * 2.0 ** -24
+        tol = 2.0 ** -24 * ref.abs() + 2 * v.abs().max() * (ez + 2.0 ** -20)
+        assert ((out[b, 0].double() - ref).abs() <= tol).all()

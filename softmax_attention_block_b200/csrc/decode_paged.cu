@@ -256,9 +256,11 @@ __global__ void __launch_bounds__(OwnCfg<T, D>::NT, 1) decode_own_kernel(PagedSt
         Cursor pc = cc;
         int tab_b = -1, tab_at = 0, tab = -1;  // 32 entries of row tab_b's table, one a lane
         // Values are not touched again before the next step; letting go of them first leaves L2 to the
-        // keys on their way back (32 rows of 1 to 8192, 32 heads of 128: 594 -> 579 us). With rows of
-        // 128 bytes (253 -> 256) or behind a prefix (154 -> 156) the hint costs more than it gives.
-        constexpr bool HINT = C::ROW > 128 && !SHARED;
+        // keys on their way back (bf16, 32 rows of 32 heads of 128: 598 -> 580 us for 1 to 8192 tokens,
+        // 161 -> 155 for 1 to 2000, 64.6 -> 65.0 for 1 to 700). At head dim 64 (251 -> 256 us for 48 rows
+        // of 500 to 6000, 24 heads), at fp32 (16 rows of 500 to 6000: 172 -> 174 us for 24 heads of 64, 223
+        // -> 224.5 for 16 of 128) or behind a prefix (202 -> 204) the hint costs more than it gives.
+        constexpr bool HINT = sizeof(T) == 2 && D == 128 && !SHARED;
         const uint64_t once = HINT ? tc::l2_evict_first() : 0;
         bool begun = false;
         float p_beta = 0.f, p_lf = 0.f;

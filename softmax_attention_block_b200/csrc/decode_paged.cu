@@ -575,8 +575,10 @@ __global__ void __launch_bounds__(OwnCfg<T, D>::NT, 1) decode_own_kernel(PagedSt
 // One (batch row, head): the pieces of its own part in block order, then the prefix's in block
 // order. Their weights are worked out by the threads side by side, a batch of pieces at a time;
 // then each thread adds up one output element over its share of them, its loads in flight together.
-// NT = D threads where there are many units of few pieces (96 x 24: 5 us of 121 less than with
-// 256), 256 where there are few units, which then have many (9 x 6, 33 pieces: 2 us less).
+// NT = D threads where there are many units of few pieces, 256 where there are few units, which
+// then have many (9 x 6, 33 pieces: 2 us less). Behind 8192 tokens, heads of 64, a step takes with
+// D and with 256: 39.8 and 38.2 us at 192 units, 50.6 and 50.0 at 512, 59.4 and 58.6 at 768, 67.9 and
+// 70.7 at 1152, 91.5 and 98.5 at 2048; heads of 128 or no prefix alike, within 2%.
 template <typename T, int D, bool SHARED, int NT>
 __global__ void __launch_bounds__(NT) decode_join_kernel(PagedStep a, PagedScratch s, PagedPlan p)
 {
@@ -700,7 +702,7 @@ cudaError_t run(const PagedStep &a, const PagedPlan &p, const PagedScratch &s, c
     }
     Stage stage("decode_join", st);
     const int units = a.B * a.H;
-    if (units > 2 * sm_count()) return launch_overlapped(decode_join_kernel<T, D, SHARED, D>, units, D, 0, st, a, s, p);
+    if (units > 6 * sm_count()) return launch_overlapped(decode_join_kernel<T, D, SHARED, D>, units, D, 0, st, a, s, p);
     return launch_overlapped(decode_join_kernel<T, D, SHARED, 256>, units, 256, 0, st, a, s, p);
 }
 

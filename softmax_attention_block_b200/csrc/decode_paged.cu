@@ -724,8 +724,14 @@ PagedPlan paged_plan(int B, int H, int max_pages, int page, int d, int dt, int p
     p.own_blocks = (int)(blocks < sms ? blocks : sms);
     p.own_slots = p.own_blocks + B * H;
     // bf16: the prefix is read once for up to 64 queries (48 at d = 128: shared memory), tiles of even
-    // size (their softmax is what can take longer than the loads); fp32: tiles of the CUDA-core kernel
-    p.q_tile = dt == BF16 ? ceil_div(ceil_div(B, ceil_div(B, d == 64 ? 64 : 48)), 16) * 16 : B <= 16 ? 16 : 32;
+    // size (their softmax is what can take longer than the loads); fp32: tiles of 32 on CUDA cores, of
+    // 16 for few rows. Behind 16384 tokens, 8 heads, a step takes with 16 and with 32: at d = 128 72.5 and
+    // 93.4 us for 12 rows, 73.0 and 95.2 for 16, 115.5 and 95.4 for 17; at d = 64 54.1 and 56.6 for 4
+    // rows, 60.2 and 56.7 for 8, 73.0 and 59.5 for 16. Behind 2047 they are even at d = 64.
+    if (dt == BF16)
+        p.q_tile = ceil_div(ceil_div(B, ceil_div(B, d == 64 ? 64 : 48)), 16) * 16;
+    else
+        p.q_tile = B <= (d == 64 ? 4 : 16) ? 16 : 32;
     p.q_tiles = ceil_div(B, p.q_tile);
     p.key_tile = dt == BF16 ? 128 : 64;
     p.key_tiles = (int)(((long long)prefix_len + p.key_tile - 1) / p.key_tile);

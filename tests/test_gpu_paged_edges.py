@@ -396,3 +396,40 @@ def test_an_infinite_key_of_an_fp32_prefix(P):
         ez = scale * q.norm() * k.norm(dim=-1).max() * 8 * math.sqrt(d) * 2.0 ** -24
         tol = 2.0 ** -24 * ref.abs() + 2 * v.abs().max() * (ez + 2.0 ** -20)
         assert ((out[b, 0].double() - ref).abs() <= tol).all()
+
+
+def test_tables_of_a_large_pool(P):
+    """300003 pages: reserve gives the lowest free pages in the order of its list, compaction fills the
+    lowest gaps with the used pages behind them."""
+    N, R, M, page = 300003, 200, 1700, 16
+    rng = torch.Generator().manual_seed(0)
+    used = torch.randperm(N, generator=rng)[: R * 1200].view(R, 1200).int()
+    table = torch.full((R, M), -1, dtype=torch.int32)
+    table[:, :1200] = used
+    owner = torch.full((N,), -1, dtype=torch.int32)
+    owner[used.long()] = (torch.arange(R)[:, None] * M + torch.arange(1200)).int()
+    held = torch.full((R,), 1200, dtype=torch.int32)
+    rows, more = torch.randperm(R, generator=rng)[:150], torch.randint(0, 300, (150,), generator=rng)
+    dev = [t.cuda() for t in (table, held, owner)]
+    tokens = (1200 + more) * page - torch.randint(0, page, (150,), generator=rng) * (more > 0)
+    info = P.path_pages_reserve(*dev, page, rows.int().cuda(), tokens.int().cuda())
+    free = (owner < 0).nonzero().flatten()
+    total = int(more.sum())
+    assert info.tolist() == [0, 0, R * 1200 + total, total]
+    at = 0
+    for r, m in zip(rows.tolist(), more.tolist()):
+        table[r, 1200:1200 + m] = free[at:at + m].int()
+        owner[free[at:at + m]] = (r * M + 1200 + torch.arange(m)).int()
+        held[r] += m
+        at += m
+    for a, b in zip(dev, (table, held, owner)):
+        assert torch.equal(a.cpu(), b)
+    moves, info = P.path_pages_compact(dev[0], dev[1], dev[2])
+    n = int((owner >= 0).sum())
+    src, dst = n + (owner[n:] >= 0).nonzero().flatten(), (owner[:n] < 0).nonzero().flatten()
+    assert info.tolist() == [0, len(src), n, 0]
+    assert torch.equal(moves[: len(src)].cpu(), torch.stack([src, dst], 1).int())
+    table.view(-1)[owner[src].long()] = dst.int()
+    owner[dst] = owner[src]
+    owner[src] = -1
+    assert torch.equal(dev[0].cpu(), table) and torch.equal(dev[2].cpu(), owner)

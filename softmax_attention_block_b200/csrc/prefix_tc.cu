@@ -18,9 +18,11 @@
 // 8 steps for O^T with the parts side by side as columns.
 //
 // A step cuts the sum so far to 24 bits instead of rounding it, so a long O^T would drift towards
-// zero (832 steps: by 3.4e-5 of the weights' sum). Every 8 tiles the softmax warps therefore add its
-// parts to a total in tensor memory, in rounded fp32, and start them from zero (0.8e-6; 121 -> 123 us
-// for the step of 96 x 24 heads of 64 below, every 4 tiles 126 us; 156 -> 157 us at 32 x 32 of 128).
+// zero (832 steps: by 3.4e-5 of the weights' sum). Every 8 tiles (4 at D = 128) the softmax warps
+// therefore add its parts to a total in tensor memory, in rounded fp32, and start them from zero
+// (0.8e-6 every 8). For the step of 96 x 24 heads of 64 below, never, every 8 and every 4 tiles take
+// 121, 123 and 126 us; at 32 x 32 of 128 156.2, 157.0 and 157.4, and 1.3, 0.62 and 0.37 e-4 of the
+// output's norm differ from 64 bits rounded once.
 //
 // The running maximum of a query is a reference that moves only when a logit
 // passes it by more than 2^8 (or at a unit's first tile): then the warps that
@@ -57,7 +59,6 @@ constexpr int PARTS = PREFIX_PARTS;  // bf16 numbers that make an fp32 one
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LOW = -1e30f;  // reference of a query that has no weight yet
 constexpr float SLACK = 8.f;
-constexpr int FOLD = 8;  // tiles after which O^T's parts are added to its total
 
 // GROUPS softmax groups: units of QT = 16 GROUPS queries, QN the distance of the two S^T.
 template <int D, int GROUPS>
@@ -77,6 +78,7 @@ struct Cfg {
     static constexpr int NBAR = 2 * NK + 2 * NV + 9;
     static constexpr int SMEM = BAR_OFF + NBAR * 8 + 16 + 1024;
     static constexpr int T_S = 0, T_O = 2 * QN, T_T = T_O + PARTS * QT, T_END = T_T + QT;  // two S^T, O^T for hi | mid | lo, its total
+    static constexpr int FOLD = D == 64 ? 8 : 4;  // tiles after which O^T's parts are added to its total
     static constexpr int TMEM = T_END <= 128 ? 128 : T_END <= 256 ? 256 : 512;
     static_assert(SMEM <= 232448, "shared memory");
 };
@@ -401,7 +403,7 @@ __global__ void __launch_bounds__(Cfg<D, GROUPS>::NT, 1)
 #pragma unroll
                     for (int i = 0; i < CN; i += 2) asm("max.f32 %0, %0, %1, %2;" : "+f"(top) : "f"(z[i]), "f"(z[i + 1]));
                 }
-                if (group_any(grp, first || n % FOLD == 0 || top > SLACK)) {
+                if (group_any(grp, first || n % C::FOLD == 0 || top > SLACK)) {
                     logits();
                     const float mine = warp_reduce<false>(z);
                     if (lane < CN) sR[(warp % 4) * QN + c0 + lane] = mine;

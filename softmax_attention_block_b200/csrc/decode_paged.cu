@@ -6,8 +6,9 @@
 //
 // Bound by HBM: it reads K and V once and writes K once (3 d elements a row and
 // head) for about 8 d operations. 48 rows of 500 to 6000 tokens, 24 heads of 64,
-// bf16 with the gate: 249 us for 1475 MB, 5.9 TB/s (90% of a plain copy); 32 rows
-// of 1 to 8192, 32 heads of 128: 579 us for 3331 MB, 5.8 TB/s (88%).
+// bf16 with the gate: 250 us for 1475 MB, 5.9 TB/s (90% of a plain copy); 32 rows
+// of 1 to 8192, 32 heads of 128: 580 us for 3331 MB, 5.7 TB/s (88%); fp32, 16 rows of
+// 500 to 6000, 24 heads of 64: 172 us for 976 MB, 5.7 TB/s (87%). Another card was 3 to 8% slower.
 //
 // Rows differ in length, so the (row, head) units are cut into granules of 16 rows
 // and the list of all granules is dealt out to the warps in equal contiguous shares
@@ -35,9 +36,9 @@ template <typename T, int D>
 struct OwnCfg {
     // Warps of a block, and how many of them work when there is much to do. Rows of 128 bytes take
     // more instructions a byte, and the shares of short sequences wait for one another: twelve warps
-    // instead of eight there (109 us instead of 117 for 96 rows of 0 to 512 tokens behind a prefix, 24
-    // heads of 64). Long shares are bound by HBM, whose rate falls with the number of streams (283 us
-    // instead of 246 for 48 rows of 500 to 6000). Even at about 45 granules for each of eight warps.
+    // instead of eight there (122 us instead of 129 for 96 rows of 0 to 512 tokens behind a prefix, 24
+    // heads of 64). Long shares are bound by HBM, whose rate falls with the number of streams (288 us
+    // instead of 250 for 48 rows of 500 to 6000). Even at about 45 granules for each of eight warps.
     static constexpr int WARPS = D * sizeof(T) == 128 ? 12 : 8, FEW = 8, NT = 32 * WARPS;
     static constexpr int LONG_SHARE = 40;
     static constexpr int LPR = D / 16, RPP = 32 / LPR;

@@ -38,11 +38,10 @@
 // a single warp takes longer to issue a tile's MMAs than the tensor cores to do them.
 // Waits are bounded; one that gives up makes its pieces NaN and is reported.
 //
-// 32 queries, 32 heads of 128, 16384 keys: 51 us for 268 MB (5.3 TB/s; the startup is 6 of
-// them). 96 queries, 24 heads of 64, gate: 52 us, where the softmax of two tiles of 48 queries
-// takes 1.1 us a tile of keys: 150 cycles for the wait, 350 for the logits, 100 to agree that
-// the reference stays, 580 for the weights (16 exponentials a thread, and three warps share
-// the unit for them), 80 to hand them over.
+// 32 queries, 32 heads of 128, 16384 keys: 58 us for 268 MB, DRAM 58% and the tensor pipe 23%
+// busy (51 us with two parts). 96 queries, 24 heads of 64, gate: 59 us, DRAM 24%, tensor pipe 37%
+// and half of the issue slots busy: nothing is full, a tile of keys and 48 queries takes 1.3 us, the
+// chain of its logits, agreement, weights and product.
 #include "paged.cuh"
 #include "runtime.cuh"
 #include "tc.cuh"

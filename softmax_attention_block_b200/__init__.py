@@ -214,8 +214,14 @@ def _check_attn_inputs(q, k, v, w, beta, log_f):
     _expect("log_f", log_f, (B, H, L), torch.float32)
 
 
+# the current stream's handle without a Stream object around it, where this torch offers that
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream():
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    if _raw_stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(torch.cuda.current_device())
 
 
 def _workspace(nbytes, device, ws):

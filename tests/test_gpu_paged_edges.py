@@ -433,3 +433,17 @@ def test_tables_of_a_large_pool(P):
     owner[dst] = owner[src]
     owner[src] = -1
     assert torch.equal(dev[0].cpu(), table) and torch.equal(dev[2].cpu(), owner)
+
+
+def test_the_current_stream_by_either_way(P, monkeypatch):
+    """The handle that the calls get is the current stream's, with torch's short way to it and without."""
+    s = torch.cuda.Stream()
+    for stream in (torch.cuda.default_stream(), s):
+        with torch.cuda.stream(stream):
+            assert P._stream() == stream.cuda_stream
+            with monkeypatch.context() as m:
+                m.setattr(P, "_raw_stream", None)
+                assert P._stream() == stream.cuda_stream
+                c = Cache([20], 2, 64, 16, BF, False)
+                before, x = c.snap(), c.step_inputs()
+                c.check(before, x, c.call(P, x))

@@ -262,9 +262,9 @@ path_status path_decode_step_gated(const void *q, const void *k_new, const void 
  * written. Every row of the batch is carried to position L-1: where sequences of
  * different lengths are padded to one L, beta = 0 and log_f = 0 behind a row's
  * end (and finite q, k, v, w) leave its keys and biases as they are there; with
- * anything else the padding's factors are in them. Requires d in {64, 128} (the decode head dims; else
- * PATH_ERR_UNSUPPORTED) and L <= capacity (else PATH_ERR_INVALID_ARG). The
- * caches must not alias the inputs.
+ * anything else the padding's factors are in them. Requires d in {64, 128} (the
+ * decode head dims; else PATH_ERR_UNSUPPORTED) and L <= capacity (else
+ * PATH_ERR_INVALID_ARG). The caches must not alias the inputs.
  */
 path_status path_attn_prefill(const void *q, const void *k, const void *v, const void *w,
                               const float *beta, const float *log_f, float scale, int B, int H,
